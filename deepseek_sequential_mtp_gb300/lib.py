@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libmtp.so")
 
 MTP_F32, MTP_BF16 = 0, 1
 DEN = {"fixed": 0, "masked_mean": 1, "sum": 2, "global": 3, "weighted_pair": 4}
+LOGITS_STATUS = {0: "ok", 1: "empty", 2: "invalid_logits", 3: "invalid_param"}
 VERIFY_STATUS = {0: "ok", 1: "invalid_draft", 2: "zero_residual", 3: "invalid_probs",
                  4: "invalid_budget"}
 
@@ -57,6 +58,12 @@ class Fp8Matrix(ctypes.Structure):
 
 class BlockFp8(ctypes.Structure):
     _fields_ = [(k, Fp8Matrix) for k in FP8_LINEAR_MAPS]
+
+
+class LogitsParams(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("temperature", "repetition", "frequency", "presence", "hist",
+                                               "hist_len", "prompt_len", "draft", "bias_ids", "bias", "mask")] + \
+               [("hist_cap", ctypes.c_int), ("n_bias", ctypes.c_int)]
 
 
 _lib = None
@@ -127,6 +134,9 @@ def load() -> ctypes.CDLL:
     lib.mtp_diag_verify_starved.restype = i32
     lib.mtp_diag_verify_starved.argtypes = [i32, i32, i32, vp, vp, vp, u64, u64, vp, vp, vp, vp,
                                             ctypes.c_longlong, vp]
+    lib.mtp_logits_probs.restype = i32
+    lib.mtp_logits_probs.argtypes = [i32, i32, i32, i32, vp, ctypes.c_longlong, ctypes.POINTER(LogitsParams), vp, vp,
+                                     vp]
     lib.mtp_kernel_launches.restype = ctypes.c_ulonglong
     lib.mtp_kernel_launches.argtypes = []
     _lib = lib
@@ -155,6 +165,35 @@ def _need(t: torch.Tensor, name: str, dtype: torch.dtype):
         raise MtpError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise MtpError(f"{name} must be contiguous")
+
+
+def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device):
+    """Address of an optional dense argument of the given type, shape and device (None = null)."""
+    if t is None:
+        return None
+    _need(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise MtpError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.device != device:
+        raise MtpError(f"{name} is on {t.device}, not on {device}")
+    return t.data_ptr()
+
+
+def _launch_device(t: torch.Tensor, stream):
+    """The device of a call's tensors; it has to be the current one, and the stream's."""
+    dev = t.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device() or (
+            stream is not None and stream.device != dev):
+        raise MtpError(f"the tensors are on {dev}: make it the current device and use a stream of it")
+    return dev
+
+
+def _empty(shape, dtype, device, stream):
+    """An output or workspace whose memory belongs to the launching stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def check_errors(stream=None) -> int:
@@ -211,6 +250,64 @@ def verify_starved(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, seed: 
                                         _ptr(out["accepted"]), _ptr(out["next_token"]), _ptr(out["n_emit"]),
                                         _ptr(out["status"]), int(wait_limit_cycles), _stream(stream))
     _check(st, "mtp_diag_verify_starved")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Logits to probability rows
+# --------------------------------------------------------------------------
+def logits_probs(logits: torch.Tensor, temperature=None, hist=None, hist_len=None, prompt_len=None, draft=None,
+                 repetition=None, frequency=None, presence=None, bias_ids=None, bias=None, mask=None,
+                 out: Optional[dict] = None, stream=None) -> dict:
+    """Probability rows from logits [R, L, V] (f32 or bf16; rows may be a fixed
+    distance apart) under each request's penalties, biases, grammar mask and
+    temperature (include/mtp.h: mtp_logits_probs).  Returns {"p": [R, L, V]
+    float32, "status": [R, L] int32}; ``out`` may supply them, and out["p"] may
+    be the float32 logits themselves."""
+    if logits.dim() != 3:
+        raise MtpError("logits must be [R, L, V]")
+    R, L, V = logits.shape
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise MtpError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    dev = _launch_device(logits, stream)
+    sr, sl, sv = logits.stride()
+    ld = sl if L > 1 else sr if R > 1 else V
+    if R * L > 0 and ((V > 1 and sv != 1) or (R > 1 and L > 1 and sr != L * ld) or ld < V):
+        raise MtpError("logits must have dense rows a fixed distance apart")
+    prm = LogitsParams()
+    f32, i32 = torch.float32, torch.int32
+    prm.temperature = _arg(temperature, "temperature", f32, (R,), dev)
+    prm.repetition = _arg(repetition, "repetition", f32, (R,), dev)
+    prm.frequency = _arg(frequency, "frequency", f32, (R,), dev)
+    prm.presence = _arg(presence, "presence", f32, (R,), dev)
+    if hist is not None:
+        if hist.dim() != 2:
+            raise MtpError("hist must be [R, capacity]")
+        prm.hist_cap = hist.shape[1]
+        prm.hist = _arg(hist, "hist", i32, (R, prm.hist_cap), dev)
+        prm.hist_len = _arg(hist_len, "hist_len", i32, (R,), dev)
+        prm.prompt_len = _arg(prompt_len, "prompt_len", i32, (R,), dev)
+    elif hist_len is not None or prompt_len is not None:
+        raise MtpError("hist_len and prompt_len need hist")
+    if draft is not None:
+        prm.draft = _arg(draft, "draft", i32, (R, L - 1), dev)
+    if (bias_ids is None) != (bias is None):
+        raise MtpError("bias_ids and bias come together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise MtpError("bias_ids must be [R, n]")
+        prm.n_bias = bias_ids.shape[1]
+        prm.bias_ids = _arg(bias_ids, "bias_ids", i32, (R, prm.n_bias), dev)
+        prm.bias = _arg(bias, "bias", f32, (R, prm.n_bias), dev)
+    prm.mask = _arg(mask, "mask", i32, (R, L, (V + 31) // 32), dev)
+    if out is None:
+        out = {"p": _empty((R, L, V), f32, dev, stream), "status": _empty((R, L), i32, dev, stream)}
+    else:
+        _arg(out["p"], "out['p']", f32, (R, L, V), dev)
+        _arg(out["status"], "out['status']", i32, (R, L), dev)
+    st = load().mtp_logits_probs(R, L, V, MTP_F32 if logits.dtype == f32 else MTP_BF16, logits.data_ptr(), ld,
+                                 ctypes.byref(prm), out["p"].data_ptr(), out["status"].data_ptr(), _stream(stream))
+    _check(st, "mtp_logits_probs")
     return out
 
 

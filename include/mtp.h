@@ -88,6 +88,15 @@ enum {
                                      device error word's MTP_DEVERR_TIMEOUT)  */
 };
 
+/* Per-row status written by mtp_logits_probs (rows that are not OK are all zero). */
+enum {
+  MTP_LOGITS_OK = 0,
+  MTP_LOGITS_EMPTY = 1,        /* no allowed token has a logit above -inf      */
+  MTP_LOGITS_INVALID = 2,      /* an allowed token's logit is NaN or +inf      */
+  MTP_LOGITS_INVALID_PARAM = 3 /* temperature < 0, repetition <= 0, or one of
+                                  the request's parameters is not finite       */
+};
+
 /* Bits of the device error word. */
 enum {
   MTP_DEVERR_TOKEN_RANGE = 1u,  /* a token id outside [0, V) was read (clamped) */
@@ -250,6 +259,58 @@ mtp_status spec_verify(int R, int gamma, int V, const float* p, const float* q,
                        const int32_t* eos, const int32_t* remaining,
                        int32_t* accepted, int32_t* next_token, int32_t* n_emit,
                        int32_t* status, cudaStream_t stream);
+
+/* What shapes a request's distribution besides its logits; every pointer is a
+ * nullable DEVICE pointer, 4-byte aligned.  Per request r (float [R]):
+ *   temperature (default 1; 0 = greedy), repetition (default 1), frequency and
+ *   presence (default 0).
+ *   hist [R, hist_cap] int32: the request's tokens, of which the first
+ *   hist_len[r] count (default hist_cap; clamped to [0, hist_cap]) and of those
+ *   the first prompt_len[r] are the prompt (default 0).  Ids outside [0, V) are
+ *   passed over.
+ *   draft [R, L-1] int32: tokens that precede row (r, j): draft[r, 0..j-1].
+ *   bias_ids [R, n_bias] int32, bias [R, n_bias] float: added to the logits of
+ *   those ids (ids outside [0, V) are passed over; of entries with the same id
+ *   the last one holds).
+ *   mask [R, L, ceil(V/32)] uint32: bit v % 32 of word v / 32 allows token v.
+ * hist_cap <= 262144, n_bias <= 4095. */
+typedef struct mtp_logits_params {
+  const float* temperature;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* hist;
+  const int32_t* hist_len;
+  const int32_t* prompt_len;
+  const int32_t* draft;
+  const int32_t* bias_ids;
+  const float* bias;
+  const uint32_t* mask;
+  int hist_cap;
+  int n_bias;
+} mtp_logits_params;
+
+/* Logits to probability rows: the p (or q) that spec_verify takes, under each
+ * request's sampling parameters and grammar.  Row (r, j), j = 0..L-1, is the
+ * position after the request's tokens and draft[r, 0..j-1] (L = gamma + 1 for
+ * verification).  With n(v) the occurrences of v among the generated tokens
+ * (hist from prompt_len on, and the row's drafts), and seen(v) whether v occurs
+ * among them or in the prompt:
+ *   z(v) = seen(v) ? (x(v) > 0 ? x(v) / repetition : x(v) * repetition) : x(v)
+ *   z(v) -= frequency * n(v) + presence * [n(v) > 0];  z(v) += bias(v)
+ *   z(v) = -inf where the mask does not allow v
+ *   p = softmax(z / temperature), or at temperature 0 the one-hot row of the
+ *   lowest index of the maximum.
+ * Masked logits may hold anything; an allowed -inf is a probability of 0.
+ *   logits: R * L rows of V elements (dtype MTP_F32 or MTP_BF16), ld elements
+ *   apart (ld >= V); p [R, L, V] float (p may be the logits' own buffer when
+ *   dtype is MTP_F32 and ld == V, and must not overlap them otherwise);
+ *   status [R, L] int32 nullable = MTP_LOGITS_*; a row that is not OK is zero,
+ *   which spec_verify reports as MTP_VERIFY_ZERO_RESIDUAL where it draws from
+ *   it.  prm nullable (a plain softmax).  V <= 524288, L <= 65536.
+ * Each row is read and written once; no workspace. */
+mtp_status mtp_logits_probs(int R, int L, int V, int dtype, const void* logits, long long ld,
+                            const mtp_logits_params* prm, float* p, int32_t* status, cudaStream_t stream);
 
 /* Gradient buffers of the training step (fp32, device, same shapes as the
  * corresponding weights; the step ADDS into them, so the caller zeroes them

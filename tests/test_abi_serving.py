@@ -1,0 +1,38 @@
+"""Host validation of the serving operators' C entries (no launches, no GPU)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from deepseek_sequential_mtp_gb300 import build, lib as binding
+    build.build()
+    return binding.load()
+
+
+FAKE = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+def test_logits_probs_host_validation(lib):
+    from deepseek_sequential_mtp_gb300 import lib as binding
+
+    def call(R=2, L=2, V=100, dtype=0, logits=FAKE, ld=100, p=ctypes.c_void_p(1 << 24), status=None, **prm):
+        s = binding.LogitsParams()
+        for k, v in prm.items():
+            setattr(s, k, v)
+        return lib.mtp_logits_probs(R, L, V, dtype, logits, ld, ctypes.byref(s), p, status, None)
+
+    assert call(R=-1) == 1 and call(L=0) == 1 and call(V=0) == 1 and call(dtype=5) == 1
+    assert call(R=0, logits=None, p=None) == 0
+    assert call(logits=None) == 1 and call(p=None) == 1
+    assert call(V=524289, ld=524289) == 7 and call(L=65537) == 7
+    assert call(ld=99) == 2
+    assert call(logits=ODD) == 3 and call(p=ODD) == 3 and call(status=ODD) == 3 and call(mask=(1 << 20) + 1) == 3
+    assert call(dtype=1, logits=ctypes.c_void_p((1 << 20) + 1)) == 3
+    assert call(p=FAKE, ld=104) == 1 and call(p=FAKE, dtype=1) == 1  # in place with gaps, or over bf16 logits
+    assert call(hist_cap=-1) == 1 and call(n_bias=-1) == 1
+    assert call(hist_cap=4) == 1 and call(n_bias=3, bias=1 << 20) == 1
+    assert call(hist_cap=262145, hist=1 << 20) == 7 and call(n_bias=4096, bias=1 << 20, bias_ids=1 << 20) == 7
+    assert call(R=1 << 20, L=1 << 10) == 7
