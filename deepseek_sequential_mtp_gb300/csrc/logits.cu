@@ -9,36 +9,46 @@
 //   z(v) -= freq n(v) + pres [n(v) > 0];  z(v) += bias(v);  z(v) = -inf where the mask bit is 0
 //   p = softmax(z / temperature), or the one-hot of the lowest index of the maximum at temperature 0.
 //
-// Bound: HBM.  A row is read once and written once (4 or 2 bytes in, 4 out, one
-// mask bit).  A cluster of C CTAs holds the row in registers (kThreads x 4 NV
-// values per CTA), so the maximum and the sum need one exchange: every CTA
-// forms e = exp((z - m_c) / T) against its own maximum m_c, sums it, and sends
-// (m_c, s_c) to the cluster's CTAs, after which each scales its values by
-// exp((m_c - M) / T) / S.  Sums are fp32 over at most 64 values per thread
-// and a tree above that.
+// Bound: HBM.  A row is read once (4 or 2 bytes a value and one mask bit) and
+// written once (4 bytes).  A cluster of C CTAs takes a row, each CTA a slice:
+// pass 1 streams the slice and keeps a running maximum and sum per thread,
+// the cluster exchanges (maximum, sum), and pass 2 streams the slice again,
+// out of L2 (or out of registers, where one batch of loads covers it), and
+// writes p.  Holding the slices in registers instead reads nothing twice but
+// leaves two CTAs per SM that wait for one phase after the other (120 us on
+// 320 rows of 129280 bf16 logits with a 2048-token history, mask and biases;
+// this form 76 us, 3.4 TB/s, and 59 us without penalties; a streaming copy of
+// the same bytes 41 us).  What is left is the latency of the marking's phases.
 //
-// Penalties and biases are sparse, the row is dense: one 32-bit word of shared
-// memory per vocabulary entry of the CTA's slice collects them -- bits 0-18
-// count the generated occurrences, bit 19 marks any occurrence, bits 20-31
-// hold 1 + the index of the request's bias entry (the last entry of an id
-// wins) -- by integer atomics, whose order cannot change the result.  The
-// history is scanned while the row's loads are in flight.
+// Penalties and biases are sparse, the row is dense.  A bit per vocabulary
+// entry of the slice marks the ids that occur; the ranks of the set bits
+// number them, and one 32-bit word per marked id collects what happens to it
+// -- bits 0-18 count the generated occurrences, bit 19 marks any occurrence,
+// bits 20-31 hold 1 + the index of the request's bias entry (the last entry of
+// an id wins) -- by integer atomics, whose order cannot change the result.
+// One thread per marked id forms its z; both passes leave these ids out, by
+// the same bits as the grammar's, and their p are written last.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 
 #include "common.cuh"
-#include "mbarrier.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 512;
+// 256 threads with four vectors in flight, five CTAs per SM: over (threads,
+// vectors, CTAs per SM) = (512, 8, 2), (512, 4, 3), (1024, 2, 2) this one was
+// fastest on 320 rows of 129280 (76 us; 78, 80, 84) and within 2 us on few rows.
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 5;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;                 // 4-value vectors a thread has in flight
+constexpr int kBatchValues = kBatch * 4 * kThreads;
 constexpr int kMaxCluster = 16;
-constexpr int kMaxNV = 16;                                         // 4-value vectors per thread
-constexpr int kMaxVocab = kMaxCluster * kMaxNV * 4 * kThreads;     // 524288
+constexpr int kMaxVocab = 524288;                // as spec_verify
+constexpr int kTargetSlice = 32768;              // entries of a CTA's slice where there are rows enough
 constexpr uint32_t kSeenBit = 1u << 19, kCountMask = kSeenBit - 1;
 constexpr int kBiasShift = 20, kMaxBias = (1 << 12) - 1;
 constexpr int kMaxHist = 1 << 18;  // hist_cap + drafts stay below the 19-bit count
@@ -50,259 +60,333 @@ struct Args {
   float* p;
   int32_t* status;
   mtp_logits_params prm;
-  int L, V, slice, use_words, has_pen;
+  int L, V, slice, slots, has_pen, sparse, live;
 };
 
-// what a CTA tells its cluster about its slice
+// what a thread, a warp, a CTA knows about its values: their maximum, the sum
+// of their exponentials against it (NaN where one of them is NaN or +inf) and,
+// in greedy rows, the lowest index of the maximum
 struct Part {
   float m, s;
-  int best;  // lowest index of the maximum (greedy rows)
-  int bad;   // a NaN or +inf among the allowed logits
+  int best;
 };
 
-__device__ __forceinline__ float exp_scaled(float x) {  // e^x
+__device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float (&v)[4]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 f = *reinterpret_cast<const float4*>(p);
-    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-  } else {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = mtp::unpack2_bf16(u.x), b = mtp::unpack2_bf16(u.y);
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+// four values as they are stored: 16 bytes of fp32 or 8 of bf16
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ void get(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void get(float (&f)[4]) const {
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xFFFF0000u);
   }
-}
+};
 
-// Value e of vector i of a thread is entry off(i, e) of the CTA's slice: with
-// VEC four neighbours per thread (16-byte accesses), else one entry per
-// thread and access (rows that are not 16-byte aligned).
-template <int NV, bool VEC, typename T>
-__global__ void __launch_bounds__(kThreads)
+// Vector i of batch b of a thread holds the slice's entries off(b, i, 0..3):
+// with VEC four neighbours (16-byte accesses), else entries kThreads apart
+// (rows that are not 16-byte aligned).
+template <bool VEC, typename T>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
 logits_probs_kernel(const Args a) {
-  extern __shared__ __align__(16) uint32_t words[];
-  __shared__ float s_red[kWarps];
-  __shared__ int s_redi[kWarps];
+  extern __shared__ __align__(16) uint32_t smem[];
+  __shared__ Part warp_part[kWarps];
   __shared__ Part parts[kMaxCluster];
+  __shared__ int warp_count[kWarps];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
   // the other CTAs' shared memory may be written once they have started
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const long long row = blockIdx.x / C;
-  const int r = static_cast<int>(row / a.L), j = static_cast<int>(row % a.L);
+  const long long row = blockIdx.x / static_cast<unsigned>(C);
+  const unsigned r = static_cast<unsigned>(row) / static_cast<unsigned>(a.L);
+  const int j = static_cast<int>(static_cast<unsigned>(row) - r * static_cast<unsigned>(a.L));
   const int lo = rank * a.slice;
   const int n = min(max(a.V - lo, 0), a.slice);
+  const int nw = a.slice / 32;
   const mtp_logits_params& q = a.prm;
+  uint32_t* live = smem;          // [nw] entries that the passes take: allowed and not marked
+  uint32_t* marks = live + nw;    // [nw] ids that occur, or have a bias
+  uint32_t* before = marks + nw;  // [nw] marked ids in the words before
+  uint32_t* word = before + nw;   // [slots] what happens to a marked id, later its z
+  int* token = reinterpret_cast<int*>(word + a.slots);  // [slots] its entry of the slice
 
-  auto off = [&](int i, int e) { return VEC ? (i * kThreads + t) * 4 + e : (i * 4 + e) * kThreads + t; };
+  auto off = [&](int b, int i, int e) {
+    return b * kBatchValues + (VEC ? (i * kThreads + t) * 4 + e : (i * 4 + e) * kThreads + t);
+  };
   const T* src = static_cast<const T*>(a.logits) + row * a.ld + lo;
-  float z[NV][4];
+  const uint32_t* mask = q.mask ? q.mask + row * ((a.V + 31) / 32) + lo / 32 : nullptr;
+  using Raw = typename std::conditional<VEC, Raw4<T>, float4>::type;
+  Raw raw[kBatch];
+  auto fetch = [&](int b) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if constexpr (VEC) {  // n is a multiple of 4
-      if (off(i, 0) < n) load4(src + off(i, 0), z[i]);
-      else z[i][0] = z[i][1] = z[i][2] = z[i][3] = -INFINITY;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[i][e] = off(i, e) < n ? mtp::load_f32<T>(src + off(i, e)) : -INFINITY;
+    for (int i = 0; i < kBatch; ++i) {
+      if constexpr (VEC) {  // n is a multiple of 4
+        if (off(b, i, 0) < n) raw[i] = *reinterpret_cast<const Raw*>(src + off(b, i, 0));
+      } else {
+        raw[i].x = off(b, i, 0) < n ? mtp::load_f32<T>(src + off(b, i, 0)) : -INFINITY;
+        raw[i].y = off(b, i, 1) < n ? mtp::load_f32<T>(src + off(b, i, 1)) : -INFINITY;
+        raw[i].z = off(b, i, 2) < n ? mtp::load_f32<T>(src + off(b, i, 2)) : -INFINITY;
+        raw[i].w = off(b, i, 3) < n ? mtp::load_f32<T>(src + off(b, i, 3)) : -INFINITY;
+      }
     }
-  }
+  };
+  // the live values of vector i, -inf for the others
+  auto values = [&](int b, int i, float (&z)[4]) {
+    if constexpr (VEC) {
+      const int o = off(b, i, 0);
+      raw[i].get(z);
+      uint32_t on = o < n ? 0xFu : 0u;
+      if (a.live && o < n) on = live[o >> 5] >> (o & 31);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!((on >> e) & 1u)) z[e] = -INFINITY;
+    } else {
+      z[0] = raw[i].x; z[1] = raw[i].y; z[2] = raw[i].z; z[3] = raw[i].w;
+      if (a.live) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int o = off(b, i, e);
+          if (o < n && !((live[o >> 5] >> (o & 31)) & 1u)) z[e] = -INFINITY;
+        }
+      }
+    }
+  };
+  const int batches = (n + kBatchValues - 1) / kBatchValues;
+  fetch(0);
+
   const float temp = q.temperature ? q.temperature[r] : 1.f;
   const float rep = q.repetition ? q.repetition[r] : 1.f;
   const float freq = q.frequency ? q.frequency[r] : 0.f;
   const float pres = q.presence ? q.presence[r] : 0.f;
   const bool params_ok = temp >= 0.f && temp < INFINITY && rep > 0.f && rep < INFINITY && fabsf(freq) < INFINITY &&
                          fabsf(pres) < INFINITY;
-
-  if (a.use_words) {
-    for (int i = t * 4; i < n; i += kThreads * 4) *reinterpret_cast<uint4*>(words + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (q.n_bias > 0) {
-      const int32_t* ids = q.bias_ids + static_cast<size_t>(r) * q.n_bias;
-      for (int i = t; i < q.n_bias; i += kThreads) {
-        const unsigned v = static_cast<unsigned>(ids[i]) - static_cast<unsigned>(lo);
-        if (ids[i] >= 0 && v < static_cast<unsigned>(n)) atomicMax(&words[v], static_cast<uint32_t>(i + 1) << kBiasShift);
-      }
-      __syncthreads();
-    }
-    if (a.has_pen) {
-      const int len = q.hist ? min(max(q.hist_len ? q.hist_len[r] : q.hist_cap, 0), q.hist_cap) : 0;
-      const int made = q.prompt_len ? q.prompt_len[r] : 0;  // tokens from here on were generated
-      const int32_t* h = q.hist + static_cast<size_t>(r) * q.hist_cap;
-      for (int i = t; i < len; i += kThreads) {
-        const int id = h[i];
-        const unsigned v = static_cast<unsigned>(id) - static_cast<unsigned>(lo);
-        if (id >= 0 && v < static_cast<unsigned>(n)) {
-          if (i < made) atomicOr(&words[v], kSeenBit);
-          else atomicAdd(&words[v], 1u);
-        }
-      }
-      if (q.draft) {
-        const int32_t* y = q.draft + static_cast<size_t>(r) * (a.L - 1);
-        for (int i = t; i < j; i += kThreads) {
-          const int id = y[i];
-          const unsigned v = static_cast<unsigned>(id) - static_cast<unsigned>(lo);
-          if (id >= 0 && v < static_cast<unsigned>(n)) atomicAdd(&words[v], 1u);
-        }
-      }
-      __syncthreads();
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      uint32_t w4[4];
-      if constexpr (VEC) {
-        const uint4 u = off(i, 0) < n ? *reinterpret_cast<const uint4*>(words + off(i, 0)) : make_uint4(0, 0, 0, 0);
-        w4[0] = u.x; w4[1] = u.y; w4[2] = u.z; w4[3] = u.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w4[e] = off(i, e) < n ? words[off(i, e)] : 0u;
-      }
-      if ((w4[0] | w4[1] | w4[2] | w4[3]) == 0u) continue;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t w = w4[e];
-        if (w == 0u) continue;
-        float v = z[i][e];
-        const uint32_t cnt = w & kCountMask;
-        if (w & (kSeenBit | kCountMask)) v = v > 0.f ? __fdiv_rn(v, rep) : __fmul_rn(v, rep);
-        if (cnt) v = __fsub_rn(v, __fadd_rn(__fmul_rn(freq, static_cast<float>(cnt)), pres));
-        if (w >> kBiasShift) v = __fadd_rn(v, q.bias[static_cast<size_t>(r) * q.n_bias + (w >> kBiasShift) - 1]);
-        z[i][e] = v;
-      }
-    }
-  }
-  if (q.mask) {  // a CTA's slice starts at a multiple of 32
-    const uint32_t* mw = q.mask + row * ((a.V + 31) / 32) + lo / 32;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if constexpr (VEC) {
-        const uint32_t bits = off(i, 0) < n ? mw[off(i, 0) >> 5] >> (off(i, 0) & 31) : 0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!((bits >> e) & 1u)) z[i][e] = -INFINITY;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (off(i, e) >= n || !((mw[off(i, e) >> 5] >> (off(i, e) & 31)) & 1u)) z[i][e] = -INFINITY;
-      }
-    }
-  }
-  // the slice's maximum; fmaxf drops a NaN, so the flag looks for it beside +inf
-  float m = -INFINITY;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      bad |= !(z[i][e] < INFINITY);
-      m = fmaxf(m, z[i][e]);
-    }
-  m = mtp::warp_max(m);
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    s_red[warp] = m;
-    s_redi[warp] = bad;
-  }
-  __syncthreads();
-  m = -INFINITY;
-  int any_bad = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    m = fmaxf(m, s_red[w]);
-    any_bad |= s_redi[w];
-  }
-  __syncthreads();
   const bool greedy = temp == 0.f;
-  const float inv_t = greedy ? 0.f : fminf(1.f / temp, 3.4028234e38f);
-  float sum = 0.f;
-  int best = 0x7fffffff;
-  if (!greedy) {
-    // a slice without a finite maximum has e = 0 everywhere (its z are -inf)
-    const float mz = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[i][e] = exp_scaled((z[i][e] - mz) * inv_t);
-      sum += (z[i][0] + z[i][1]) + (z[i][2] + z[i][3]);
+  const float k = fminf(1.4426950408889634f / temp, 3.4028234e38f);  // e^(x / T) = 2^(x k)
+
+  Part mine{-INFINITY, 0.f, 0x7fffffff};
+  // one value more (greedy rows keep s = NaN for a NaN or +inf)
+  auto add = [&](float z, int index) {
+    if (greedy) {
+      if (!(z < INFINITY)) mine.s = NAN;
+      if (z > mine.m || (z == mine.m && index < mine.best)) {
+        mine.m = z;
+        mine.best = index;
+      }
+    } else {
+      const float mn = fmaxf(mine.m, z), mz = mn == -INFINITY ? 0.f : mn;
+      mine.s = mine.s * ex2((mine.m - mz) * k) + ex2((z - mz) * k);
+      mine.m = mn;
     }
-    sum = mtp::warp_sum(sum);
-    if (lane == 0) s_red[warp] = sum;
-  } else {
+  };
+
+  int n_marked = 0;
+  if (a.sparse) {
+    const int len = a.has_pen && q.hist ? min(max(q.hist_len ? q.hist_len[r] : q.hist_cap, 0), q.hist_cap) : 0;
+    const int made = q.prompt_len ? q.prompt_len[r] : 0;  // tokens from here on were generated
+    const int32_t* h = q.hist + static_cast<size_t>(r) * q.hist_cap;
+    const int32_t* y = q.draft + static_cast<size_t>(r) * (a.L - 1);
+    const int n_draft = a.has_pen && q.draft ? j : 0;
+    const int32_t* ids = q.bias_ids + static_cast<size_t>(r) * q.n_bias;
+    auto entry = [&](int id) {  // index within the slice, or -1
+      const unsigned v = static_cast<unsigned>(id) - static_cast<unsigned>(lo);
+      return id >= 0 && v < static_cast<unsigned>(n) ? static_cast<int>(v) : -1;
+    };
+    auto mark = [&](int id) {
+      const int v = entry(id);
+      if (v >= 0) atomicOr(&marks[v >> 5], 1u << (v & 31));
+    };
+    for (int i = t; i < nw; i += kThreads) marks[i] = 0u;
+    for (int i = t; i < a.slots; i += kThreads) word[i] = 0u;
+    __syncthreads();
+    for (int i = t; i < len; i += kThreads) mark(h[i]);
+    for (int i = t; i < n_draft; i += kThreads) mark(y[i]);
+    for (int i = t; i < q.n_bias; i += kThreads) mark(ids[i]);
+    __syncthreads();
+    {  // ranks: every thread counts a run of words, scanned over the CTA
+      const int per = (nw + kThreads - 1) / kThreads, w0 = t * per;
+      int count = 0;
+      for (int i = w0; i < min(w0 + per, nw); ++i) {
+        const uint32_t mk = marks[i];
+        live[i] = (mask ? (i * 32 < n ? mask[i] : 0u) : 0xFFFFFFFFu) & ~mk;
+        count += __popc(mk);
+      }
+      int incl = count;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) warp_count[warp] = incl;
+      __syncthreads();
+      int base = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (z[i][e] == m && off(i, e) < n) best = min(best, lo + off(i, e));
-    best = __reduce_min_sync(0xffffffffu, best);
-    if (lane == 0) s_redi[warp] = best;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) base += warp_count[w];
+        n_marked += warp_count[w];
+      }
+      base += incl - count;
+      for (int i = w0; i < min(w0 + per, nw); ++i) {
+        before[i] = static_cast<uint32_t>(base);
+        base += __popc(marks[i]);
+      }
+    }
+    __syncthreads();
+    auto slot = [&](int v) { return before[v >> 5] + __popc(marks[v >> 5] & ((1u << (v & 31)) - 1u)); };
+    if (q.n_bias > 0) {  // before the counts: a maximum over whole words
+      for (int i = t; i < q.n_bias; i += kThreads) {
+        const int v = entry(ids[i]);
+        if (v >= 0) {
+          const uint32_t s = slot(v);
+          token[s] = v;
+          atomicMax(&word[s], static_cast<uint32_t>(i + 1) << kBiasShift);
+        }
+      }
+      __syncthreads();
+    }
+    auto count = [&](int id, uint32_t made_here) {
+      const int v = entry(id);
+      if (v >= 0) {
+        const uint32_t s = slot(v);
+        token[s] = v;
+        if (made_here) atomicAdd(&word[s], 1u);
+        else atomicOr(&word[s], kSeenBit);
+      }
+    };
+    for (int i = t; i < len; i += kThreads) count(h[i], i >= made);
+    for (int i = t; i < n_draft; i += kThreads) count(y[i], 1u);
+  } else if (a.live) {
+    for (int i = t; i * 32 < n; i += kThreads) live[i] = mask[i];
+    __syncthreads();
   }
+
+  // pass 1: maximum and sum
+  for (int b = 0; b < batches; ++b) {
+    if (b > 0) fetch(b);
+    if (!greedy) {
+      float z[kBatch][4], mb = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        values(b, i, z[i]);
+        mb = fmaxf(mb, fmaxf(fmaxf(z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3])));  // passes over a NaN
+      }
+      // A NaN makes the sum NaN, and so does +inf (inf - inf).  (z k - m k
+      // would save an instruction, but overflows for logits at the type's
+      // lowest value and for small T.)
+      const float mn = fmaxf(mine.m, mb), mz = mn == -INFINITY ? 0.f : mn;
+      float s4[4] = {mine.s * ex2((mine.m - mz) * k), 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s4[e] += ex2((z[i][e] - mz) * k);
+      mine.s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      mine.m = mn;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float z[4];
+        values(b, i, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (off(b, i, e) < n) add(z[e], lo + off(b, i, e));
+      }
+    }
+  }
+  if (a.sparse) {  // the marked ids, each step rounded once
+    __syncthreads();
+    for (int i = t; i < n_marked; i += kThreads) {
+      const uint32_t w = word[i], cnt = w & kCountMask;
+      const int v = token[i];
+      float z = mtp::load_f32<T>(src + v);
+      if (w & (kSeenBit | kCountMask)) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+      if (cnt) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(cnt)), pres));
+      if (w >> kBiasShift) z = __fadd_rn(z, q.bias[static_cast<size_t>(r) * q.n_bias + (w >> kBiasShift) - 1]);
+      if (mask && !((mask[v >> 5] >> (v & 31)) & 1u)) z = -INFINITY;
+      word[i] = __float_as_uint(z);
+      add(z, lo + v);
+    }
+  }
+  // merge: thread -> warp -> CTA -> cluster
+  auto weight = [&](float pm, float M) {  // a part without a maximum has s = 0 or NaN
+    return greedy || pm == -INFINITY ? 1.f : ex2((pm - M) * k);
+  };
+  {
+    const float m = mtp::warp_max(mine.m);
+    mine.s = mtp::warp_sum(mine.s * weight(mine.m, m));
+    mine.best = __reduce_min_sync(0xffffffffu, mine.m == m ? mine.best : 0x7fffffff);
+    mine.m = m;
+  }
+  auto merge = [&](const Part* p, int count) {
+    Part o{-INFINITY, 0.f, 0x7fffffff};
+    for (int i = 0; i < count; ++i) o.m = fmaxf(o.m, p[i].m);
+    for (int i = 0; i < count; ++i) {
+      o.s += p[i].s * weight(p[i].m, o.m);
+      if (p[i].m == o.m) o.best = min(o.best, p[i].best);
+    }
+    return o;
+  };
+  if (lane == 0) warp_part[warp] = mine;
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  if (warp == 0) {
-    if (!greedy) {
-      sum = mtp::warp_sum(lane < kWarps ? s_red[lane] : 0.f);
-    } else {
-      best = __reduce_min_sync(0xffffffffu, lane < kWarps ? s_redi[lane] : 0x7fffffff);
-    }
-    if (lane < C) {
-      Part* dst = cluster.map_shared_rank(parts, lane) + rank;
-      *dst = Part{m, sum, best, any_bad};
-    }
-  }
+  if (t < C) *(cluster.map_shared_rank(parts, t) + rank) = merge(warp_part, kWarps);
   cluster.sync();  // nobody touches another CTA's shared memory after this
-  float M = -INFINITY;
-  any_bad = 0;
-  for (int c = 0; c < C; ++c) {
-    M = fmaxf(M, parts[c].m);
-    any_bad |= parts[c].bad;
-  }
-  float factor = 0.f;
-  best = 0x7fffffff;
-  const bool row_ok = params_ok && !any_bad && M != -INFINITY;
-  if (row_ok) {
-    if (!greedy) {
-      float S = 0.f;
-      for (int c = 0; c < C; ++c)
-        if (parts[c].m != -INFINITY) S += parts[c].s * exp_scaled((parts[c].m - M) * inv_t);
-      if (m != -INFINITY) factor = exp_scaled((m - M) * inv_t) / S;
-    } else {
-      for (int c = 0; c < C; ++c)
-        if (parts[c].m == M) best = min(best, parts[c].best);
-    }
-  }
+  const Part all = merge(parts, C);
+  const bool bad = !(all.s == all.s);
+  const bool row_ok = params_ok && !bad && all.m != -INFINITY;
+
+  // pass 2
+  const float M = all.m, scale = greedy ? 1.f : 1.f / all.s;
   float* dst = a.p + row * a.V + lo;
+  for (int b = 0; b < batches; ++b) {
+    if (batches > 1) fetch(b);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float o[4];
+    for (int i = 0; i < kBatch; ++i) {
+      float z[4];
+      if (row_ok && !greedy) {
+        values(b, i, z);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = !row_ok ? 0.f : greedy ? (lo + off(i, e) == best ? 1.f : 0.f) : z[i][e] * factor;
-    if constexpr (VEC) {
-      if (off(i, 0) < n) *reinterpret_cast<float4*>(dst + off(i, 0)) = make_float4(o[0], o[1], o[2], o[3]);
-    } else {
+        for (int e = 0; e < 4; ++e) z[e] = ex2((z[e] - M) * k) * scale;
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (off(i, e) < n) dst[off(i, e)] = o[e];
+        for (int e = 0; e < 4; ++e) z[e] = row_ok && lo + off(b, i, e) == all.best ? 1.f : 0.f;
+      }
+      if constexpr (VEC) {
+        if (off(b, i, 0) < n) *reinterpret_cast<float4*>(dst + off(b, i, 0)) = make_float4(z[0], z[1], z[2], z[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (off(b, i, e) < n) dst[off(b, i, e)] = z[e];
+      }
     }
+  }
+  if (a.sparse && row_ok && !greedy) {  // over the zeros that the pass wrote for the marked ids
+    __syncthreads();
+    for (int i = t; i < n_marked; i += kThreads) dst[token[i]] = ex2((__uint_as_float(word[i]) - M) * k) * scale;
   }
   if (rank == 0 && t == 0 && a.status)
     a.status[row] = !params_ok ? MTP_LOGITS_INVALID_PARAM
-                    : any_bad  ? MTP_LOGITS_INVALID
-                    : M == -INFINITY ? MTP_LOGITS_EMPTY
-                                     : MTP_LOGITS_OK;
+                    : bad      ? MTP_LOGITS_INVALID
+                    : all.m == -INFINITY ? MTP_LOGITS_EMPTY
+                                         : MTP_LOGITS_OK;
 }
 
-template <int NV, bool VEC, typename T>
+constexpr int kMaxSmem = 200 * 1024;
+
+int smem_bytes(const Args& a) { return a.live ? 4 * (a.slice / 32) * (a.sparse ? 3 : 1) + 8 * a.slots : 0; }
+
+template <bool VEC, typename T>
 mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
   static mtp::PerDevice attr_smem, attr_cluster;
-  const int smem = a.use_words ? a.slice * 4 : 0;
-  auto kernel = logits_probs_kernel<NV, VEC, T>;
-  if (!mtp::smem_limit(attr_smem, kernel, NV * 4 * kThreads * 4)) return MTP_ERR_CUDA;
+  auto kernel = logits_probs_kernel<VEC, T>;
+  if (!mtp::smem_limit(attr_smem, kernel, kMaxSmem)) return MTP_ERR_CUDA;
   const int dev = mtp::current_device();
   if (C > 8 && dev >= 0 && (dev >= mtp::kMaxDevices || !attr_cluster.v[dev].load(std::memory_order_acquire))) {
     MTP_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
@@ -311,7 +395,7 @@ mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(rows * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem_bytes(a));
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -321,22 +405,6 @@ mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
   MTP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
   mtp::note_launch();
   return MTP_OK;
-}
-
-template <int NV, typename T>
-mtp_status launch_vec(const Args& a, long long rows, int C, bool vec, cudaStream_t st) {
-  return vec ? launch<NV, true, T>(a, rows, C, st) : launch<NV, false, T>(a, rows, C, st);
-}
-
-template <typename T>
-mtp_status launch_nv(const Args& a, long long rows, int C, int nv, bool vec, cudaStream_t st) {
-  switch (nv) {
-    case 1: return launch_vec<1, T>(a, rows, C, vec, st);
-    case 2: return launch_vec<2, T>(a, rows, C, vec, st);
-    case 4: return launch_vec<4, T>(a, rows, C, vec, st);
-    case 8: return launch_vec<8, T>(a, rows, C, vec, st);
-    default: return launch_vec<16, T>(a, rows, C, vec, st);
-  }
 }
 
 }  // namespace
@@ -378,27 +446,25 @@ extern "C" mtp_status mtp_logits_probs(int R, int L, int V, int dtype, const voi
   a.status = status;
   a.L = L;
   a.V = V;
-  a.has_pen = (q.repetition || q.frequency || q.presence) && (q.hist_cap > 0 || (q.draft && L > 1));
   if (L == 1) a.prm.draft = nullptr;
-  a.use_words = a.has_pen || q.n_bias > 0;
-  // Cluster size: the fewest CTAs that hold the row with 8 vectors per thread
-  // (16 only where 16 CTAs need it); twice as many for as long as that still
-  // leaves SMs idle and threads with more than one vector.
-  auto vectors = [&](int c) {
-    const int need = ((V + c - 1) / c + 4 * kThreads - 1) / (4 * kThreads);
-    int nv = 1;
-    while (nv < need) nv *= 2;
-    return nv;
+  a.has_pen = (q.repetition || q.frequency || q.presence) && (q.hist_cap > 0 || q.draft);
+  a.sparse = a.has_pen || q.n_bias > 0;
+  a.live = a.sparse || q.mask;
+  const int listed = (a.has_pen ? q.hist_cap + L - 1 : 0) + q.n_bias;  // marked ids at most
+  auto cut = [&](int c) {
+    a.slice = ((V + c - 1) / c + 31) / 32 * 32;
+    a.slots = a.sparse ? std::min(a.slice, listed) : 0;
   };
+  // Cluster size: slices of at most kTargetSlice entries whose marked ids fit
+  // into shared memory (65536 entries are within 5%, 16384 take 40% longer on
+  // 320 rows of 129280); then twice as many CTAs for as long as no SM gets
+  // more than two of them and every thread has more than one vector.
   int C = 1;
-  while (C < kMaxCluster && vectors(C) > 8) C *= 2;
+  for (cut(C); C < kMaxCluster && (a.slice > kTargetSlice || smem_bytes(a) > kMaxSmem); cut(C)) C *= 2;
   const int sms = mtp::sm_count_current();
-  while (C < kMaxCluster && vectors(C) > 1 && rows * C * 2 <= sms) C *= 2;
-  const int nv = vectors(C);
-  a.slice = ((V + C - 1) / C + 31) / 32 * 32;
-  if (a.slice > nv * 4 * kThreads) return MTP_ERR_UNSUPPORTED;  // not reached: both sides are multiples of 32
+  while (C < kMaxCluster && a.slice > 4 * kThreads && rows * C <= sms) cut(C *= 2);
   const bool vec = V % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) % (4 * esize)) == 0 &&
                    mtp::aligned16(p);
-  return dtype == MTP_F32 ? launch_nv<float>(a, rows, C, nv, vec, st)
-                          : launch_nv<__nv_bfloat16>(a, rows, C, nv, vec, st);
+  if (dtype == MTP_F32) return vec ? launch<true, float>(a, rows, C, st) : launch<false, float>(a, rows, C, st);
+  return vec ? launch<true, __nv_bfloat16>(a, rows, C, st) : launch<false, __nv_bfloat16>(a, rows, C, st);
 }
