@@ -60,6 +60,10 @@ class BlockFp8(ctypes.Structure):
     _fields_ = [(k, Fp8Matrix) for k in FP8_LINEAR_MAPS]
 
 
+class Int4Matrix(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
+
+
 class LogitsParams(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("temperature", "repetition", "frequency", "presence", "hist",
                                                "hist_len", "prompt_len", "draft", "bias_ids", "bias", "mask")] + \
@@ -134,6 +138,8 @@ def load() -> ctypes.CDLL:
     lib.mtp_diag_verify_starved.restype = i32
     lib.mtp_diag_verify_starved.argtypes = [i32, i32, i32, vp, vp, vp, u64, u64, vp, vp, vp, vp,
                                             ctypes.c_longlong, vp]
+    lib.mtp_gemm_int4w.restype = i32
+    lib.mtp_gemm_int4w.argtypes = [i32, i32, i32, i32, vp, ctypes.POINTER(Int4Matrix), vp, i32, vp]
     lib.mtp_logits_probs.restype = i32
     lib.mtp_logits_probs.argtypes = [i32, i32, i32, i32, vp, ctypes.c_longlong, ctypes.POINTER(LogitsParams), vp, vp,
                                      vp]
@@ -417,6 +423,42 @@ def gemm_fp8w(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, out: torch.
         ws = torch.empty(max(16, int(load().mtp_gemm_fp8w_workspace_bytes(K))), dtype=torch.uint8, device=x.device)
     _check(load().mtp_gemm_fp8w(R, N, K, _ptr(x), _ptr(q), _ptr(scale), _ptr(out), _ptr(ws), ws.numel(),
                                 _stream(stream)), "mtp_gemm_fp8w")
+    return out
+
+
+def _int4_matrix(name: str, q, scale, zero, group: int, device) -> Int4Matrix:
+    """ctypes view of one 4-bit matrix: q uint8 [N, K/2], scale bf16 and zero
+    uint8 (or None) [N, ceil(K/group)]."""
+    if q.dim() != 2 or group < 1:
+        raise MtpError(f"{name}.q must be [N, K/2] and the group positive")
+    shape = (q.shape[0], (2 * q.shape[1] + group - 1) // group)
+    m = Int4Matrix()
+    m.q = _arg(q, name + ".q", torch.uint8, q.shape, device)
+    m.scale = _arg(scale, name + ".scale", torch.bfloat16, shape, device)
+    m.zero = _arg(zero, name + ".zero", torch.uint8, shape, device)
+    return m
+
+
+def gemm_int4w(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
+               group: int = 128, out: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None):
+    """out[R, N] = x[R, K] @ W^T (added to ``out`` if ``accumulate``) with W =
+    (code - zero) * scale in groups of ``group`` along K, two codes per byte of
+    q [N, K/2] (include/mtp.h: mtp_gemm_int4w)."""
+    dev = _launch_device(x, stream)
+    m = _int4_matrix("w", q, scale, zero, group, dev)
+    _need(x, "x", torch.bfloat16)
+    N = q.shape[0]
+    if x.dim() != 2 or x.shape[1] != 2 * q.shape[1]:
+        raise MtpError("gemm_int4w: x [R, K], q [N, K/2]")
+    R, K = x.shape
+    if out is None:
+        if accumulate:
+            raise MtpError("gemm_int4w: accumulate needs out")
+        out = _empty((R, N), torch.float32, dev, stream)
+    else:
+        _arg(out, "out", torch.float32, (R, N), dev)
+    _check(load().mtp_gemm_int4w(R, N, K, group, x.data_ptr(), ctypes.byref(m), out.data_ptr(), int(accumulate),
+                                 _stream(stream)), "mtp_gemm_int4w")
     return out
 
 

@@ -400,3 +400,35 @@ def make_draft_inputs(cfg: DraftConfig, seed: int, device="cpu") -> dict:
     }
     out["pos"] = out["ctx_len"].clone()
     return out
+
+
+def quantize_int4_groups(w: torch.Tensor, group: int, symmetric: bool = True):
+    """Synthetic 4-bit checkpoint form of one [n, K] weight matrix: per row and
+    ``group`` columns a bf16 scale, and a zero point unless ``symmetric``, with
+    round-to-nearest codes of w / scale + zero in 0..15, two per byte (the even
+    column in the low half).  Returns (q uint8 [n, K/2], scale bfloat16
+    [n, ceil(K/group)], zero uint8 likewise or None) on w's device.  Input
+    generation only: the hot path reads them as given."""
+    w32 = w.float()
+    n, K = w32.shape
+    groups = -(-K // group)
+    pad = torch.zeros((n, groups * group), dtype=torch.float32, device=w.device)
+    pad[:, :K] = w32
+    g = pad.view(n, groups, group)
+    if symmetric:
+        scale = (g.abs().amax(-1) / 7.0).clamp(min=1e-8).to(torch.bfloat16)
+        zero = None
+        z = torch.full((n, groups, 1), 8.0, device=w.device)
+    else:
+        lo, hi = g.amin(-1).clamp(max=0.0), g.amax(-1).clamp(min=0.0)
+        scale = ((hi - lo) / 15.0).clamp(min=1e-8).to(torch.bfloat16)
+        zero = torch.round(-lo / scale.float()).clamp(0, 15).to(torch.uint8)
+        z = zero.float()[..., None]
+    codes = torch.round(g / scale.float()[..., None] + z).clamp(0, 15).to(torch.uint8).view(n, groups * group)[:, :K]
+    q = codes[:, 0::2] | (codes[:, 1::2] << 4)
+    return q.contiguous(), scale.contiguous(), zero
+
+
+def make_int4_block(weights: dict, group: int, symmetric: bool = True) -> dict:
+    """4-bit forms of the depth-1 module's eight linear maps of a weight dict."""
+    return {name: quantize_int4_groups(weights[name][0], group, symmetric) for name in FP8_LINEAR_MAPS}

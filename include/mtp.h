@@ -458,6 +458,28 @@ size_t mtp_gemm_fp8w_workspace_bytes(int K);
 mtp_status mtp_gemm_fp8w(int R, int N, int K, const void* x, const void* wq, const float* scale, float* out,
                          void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* One 4-bit weight matrix W [n, K] with group scales:
+ *   W[m][k] = (code[m][k] - zero[m][k/group]) * scale[m][k/group], taken exactly.
+ * q: [n, K/2] bytes, row-major, 16-byte aligned; byte j of a row holds code 2j
+ * in its low and code 2j+1 in its high half, 0..15.  scale: bf16
+ * [n, ceil(K/group)] row-major (the last group of a row may be short).  zero:
+ * bytes of the same shape, of which the low four bits count, or null: 8
+ * everywhere (symmetric codes). */
+typedef struct mtp_int4_matrix {
+  const void* q;
+  const void* scale;
+  const void* zero;
+} mtp_int4_matrix;
+
+/* Product of 1..32 tokens with a 4-bit weight matrix (the kernel the draft
+ * step uses with 4-bit weights): out[R, N] (fp32, row stride N) = x[R, K] · W^T,
+ * added to what out holds if `accumulate`.  x bf16; group 32, 64 or 128;
+ * K % 32 == 0; x and w->q 16-byte aligned.  Products are exact in fp32, sums
+ * and scales fp32, in an order fixed by the sizes: the result is the same every
+ * time.  No workspace. */
+mtp_status mtp_gemm_int4w(int R, int N, int K, int group, const void* x, const mtp_int4_matrix* w, float* out,
+                          int accumulate, cudaStream_t stream);
+
 /* Diagnostic GEMM on the same tcgen05 core the chain uses:
  * C[M,N] (bf16) = A[M,K] (bf16) · B[N,K]^T (bf16), fp32 accumulation.
  * K % 8 == 0; A, B, C 16-byte aligned. */

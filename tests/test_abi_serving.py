@@ -36,3 +36,17 @@ def test_logits_probs_host_validation(lib):
     assert call(hist_cap=4) == 1 and call(n_bias=3, bias=1 << 20) == 1
     assert call(hist_cap=262145, hist=1 << 20) == 7 and call(n_bias=4096, bias=1 << 20, bias_ids=1 << 20) == 7
     assert call(R=1 << 20, L=1 << 10) == 7
+
+
+def test_gemm_int4w_host_validation(lib):
+    from deepseek_sequential_mtp_gb300 import lib as binding
+
+    def call(R=4, N=64, K=256, group=128, x=FAKE, q=1 << 20, scale=1 << 20, zero=None, out=FAKE, w=True):
+        m = binding.Int4Matrix(q, scale, zero)
+        return lib.mtp_gemm_int4w(R, N, K, group, x, ctypes.byref(m) if w else None, out, 0, None)
+
+    assert call(w=False) == 1 and call(x=None) == 1 and call(out=None) == 1 and call(q=None) == 1 and call(scale=None) == 1
+    assert call(R=0) == 2 and call(R=33) == 2 and call(N=0) == 2 and call(K=0) == 2
+    assert call(K=40) == 3 and call(x=ODD) == 3 and call(q=(1 << 20) + 8) == 3 and call(scale=(1 << 20) + 1) == 3
+    assert call(out=ODD) == 3
+    assert call(group=48) == 7 and call(group=256) == 7
