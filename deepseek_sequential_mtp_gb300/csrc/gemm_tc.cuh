@@ -91,6 +91,12 @@ mtp_status gemm_bf16_launch(const GemmDesc& g, cudaStream_t stream);
 bool tensor_map_bf16_2d(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint64_t ld,
                         uint32_t box_cols, uint32_t box_rows, bool swizzle128);
 
+// Tensor map of a four-dimensional bf16 array (dims from the innermost, which
+// is dense; byte strides of the others, multiples of 16) for tiled loads with
+// the 128-byte swizzle (box[0] * 2 <= 128).
+bool tensor_map_bf16_4d(CUtensorMap* m, const void* ptr, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                        const uint32_t (&box)[4]);
+
 // Tensor map of a row-major byte matrix [rows, cols] (row stride ld bytes, a
 // multiple of 16) for tiled loads of box_cols x box_rows with the 128-byte
 // swizzle (box_cols <= 128).

@@ -1,0 +1,887 @@
+// Attention of a batch's new tokens over a prefix that all requests share and
+// over each request's own cache.
+//
+// o = softmax(scale q [Kp; Kr]^T) [Vp; Vr] for every (request r, token i, head):
+// Kp, Vp are the prefix, read once for the whole batch, Kr, Vr the request's own
+// rows.  The softmax is taken in parts, (maximum m, sum l, output o) per part,
+// and the parts joined at the end: o = Σ 2^(m_p - M) o_p / Σ 2^(m_p - M) l_p.
+//
+// Bound: HBM for few rows (the keys and values once: 4 hd bytes per key and
+// head), the tensor cores once some 300 rows share a head's prefix.
+//
+// All rows that see the same keys form one matrix: for the prefix the R L G rows
+// (G = query heads per key head) of all requests, for a request's own cache its
+// L G rows.  Work is cut into items -- (key head, up to 256 rows) over the prefix,
+// (request, key head, up to 256 rows) over its cache -- and an item into blocks
+// of 128 keys.  The blocks of all items, weighted by their cost, are dealt to the
+// CTAs in equal contiguous ranges, whatever the lengths; a CTA's range within an
+// item (a segment) leaves one record of partial results per row, and a second
+// kernel joins a row's records.  Both kernels work the deal out from ctx_len.
+//
+// A segment runs as in the chain's attention: TMA brings K and V blocks, S = Q K^T
+// and O += P V run on tcgen05 with S, P and O in TMEM, a softmax thread owns a
+// row.  TMEM holds two tiles (S and P share columns), each with its own
+// warpgroup.  With more than 128 rows the two tiles are rows 0-127 and 128-255
+// and share every K/V block; with up to 128 rows both tiles are the same rows
+// and take the blocks alternately, so that one's softmax runs under the other's
+// products, each with a maximum, a sum and an output of its own (two records).
+//   softmax    warps 0-3 tile 0, warps 4-7 tile 1
+//   TMA warp   lane 0 walks the deal, publishes the segments in a ring and loads
+//              K, lane 1 loads V
+//   Q warp     gathers the rows' q with cp.async into the swizzled layout
+//   MMA warp   one thread issues every product
+// Keys past a request's ctx_len may hold anything: their scores are replaced, and
+// their V rows are cleared in shared memory (0 times NaN is NaN).  Every wait is
+// bounded.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "gemm_tc.cuh"
+#include "mbarrier.cuh"
+#include "prefix_attn.cuh"
+#include "tcgen05.cuh"
+
+MTP_DEFINE_ERROR_WORD(mtp_take_errors_prefix)
+
+namespace mtp {
+namespace {
+
+constexpr int kRows = 128;   // rows per tile (MMA M, TMEM lanes)
+constexpr int kKeys = 128;   // keys per block
+constexpr float kStaleMaxLog2 = 8.0f;  // a running maximum is replaced only when exceeded by 2^8
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+// cost of a block with one row tile and with two, for the deal
+constexpr int kCostOne = 3, kCostTwo = 5;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tiled four-dimensional tensor copy global -> shared; x is the inner coordinate
+__device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// sizes of the two kinds of items, and where their records are
+struct Shape {
+  int R, L, H, Hkv, G, hd, P, T, causal;
+  int prefix_rows, prefix_tiles, prefix_blocks, prefix_cost;  // rows per key head; items per key head; ...
+  int own_rows, own_tiles, own_cost;
+  int prefix_rec, own_rec;      // record rows per segment
+  long long own_rec0;           // record row of the first own segment
+  int grid;
+  const int32_t* ctx_len;
+
+  __host__ __device__ int blocks_of(int len) const { return (len + kKeys - 1) / kKeys; }
+  __device__ __forceinline__ int ctx(int r) const { return ctx_len ? min(max(ctx_len[r], 0), T) : T; }
+  __host__ __device__ long long prefix_total() const {
+    return static_cast<long long>(Hkv) * prefix_tiles * prefix_blocks * prefix_cost;
+  }
+  // cost of one block of a request's cache over all its heads and row tiles
+  __host__ __device__ long long own_step() const { return static_cast<long long>(Hkv) * own_tiles * own_cost; }
+};
+
+// The deal: CTA k takes the blocks that start in [k total / n, (k + 1) total / n),
+// n so small that every CTA gets a block.
+struct Deal {
+  long long total;
+  int n;
+  __device__ __forceinline__ Deal(const Shape& s, long long own_blocks) {
+    total = s.prefix_total() + own_blocks * s.own_step();
+    const long long most = total / kCostTwo;
+    n = static_cast<int>(most < 1 ? 1 : most < s.grid ? most : s.grid);
+  }
+  __device__ __forceinline__ long long start(int k) const { return k * total / n; }
+  // the CTA whose range the position is in
+  __device__ __forceinline__ int owner(long long pos) const { return static_cast<int>(((pos + 1) * n + total - 1) / total - 1); }
+};
+
+// a segment: blocks [b0, b0 + n) of an item
+struct Segment {
+  int kind;  // bit 0: own cache (else prefix), bit 1: two row tiles; -1 ends
+  int head, tile, r;
+  int b0, n, keys;  // keys: of the item
+  int rec;          // index of its records among the kind's
+};
+static_assert(sizeof(Segment) == 32, "two 16-byte words in the ring");
+
+template <int HD>
+struct Cfg {
+  static constexpr int kSoftmaxWarps = 8;
+  static constexpr int kTmaWarp = 8, kQWarp = 9, kMmaWarp = 10;
+  static constexpr int kThreads = 32 * 11;
+  static constexpr int kChunks = HD / 64;
+  static constexpr int kPiece = 128 * 128;       // one [128 rows x 128 B] swizzled piece
+  static constexpr int kTileBytes = kRows * HD * 2;  // a Q, K or V tile
+  static constexpr int kQTiles = HD == 64 ? 4 : 2;
+  static constexpr int kKStages = HD == 64 ? 4 : 3;
+  static constexpr int kVStages = HD == 64 ? 4 : 2;
+  static constexpr int kOffK = kQTiles * kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+  static constexpr int kRing = 4;
+  static constexpr int kReaders = 3 + kSoftmaxWarps;  // V lane, Q warp, MMA thread, softmax warps
+  // q, k, v full/empty; per tile s_full, p_full, pv_done, o_free; drain; segment ring full/empty
+  static constexpr int kNumBars = 2 * (kQTiles + kKStages + kVStages) + 8 + 1 + 2 * kRing;
+  static constexpr int kOffRing = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffRing + 32 * kRing + 16;
+  static constexpr uint32_t kColO = 256;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(Cfg<HD>::kThreads, 1)
+prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant__ CUtensorMap pv,
+                   const __grid_constant__ CUtensorMap kk, const __grid_constant__ CUtensorMap kv, const Shape sh,
+                   const __nv_bfloat16* __restrict__ q, long long q_r, long long q_l, long long q_h, float scale_log2,
+                   float2* __restrict__ rec_ml, float* __restrict__ rec_o) {
+  using C = Cfg<HD>;
+  pdl_trigger();  // the joining kernel may start its setup
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t s0 = smem_u32(smem);
+  if (s0 & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(&g_mtp_error_word, MTP_DEVERR_TIMEOUT);
+    return;
+  }
+  const uint32_t sQ = s0, sK = s0 + C::kOffK, sV = s0 + C::kOffV, bar0 = s0 + C::kOffBar;
+  auto q_full = [&](uint32_t i) { return bar0 + 8u * (i % C::kQTiles); };
+  auto q_empty = [&](uint32_t i) { return bar0 + 8u * (C::kQTiles + i % C::kQTiles); };
+  const uint32_t bark = bar0 + 16u * C::kQTiles;
+  auto k_full = [&](uint32_t i) { return bark + 8u * (i % C::kKStages); };
+  auto k_empty = [&](uint32_t i) { return bark + 8u * (C::kKStages + i % C::kKStages); };
+  const uint32_t barv = bark + 16u * C::kKStages;
+  auto v_full = [&](uint32_t i) { return barv + 8u * (i % C::kVStages); };
+  auto v_empty = [&](uint32_t i) { return barv + 8u * (C::kVStages + i % C::kVStages); };
+  const uint32_t barx = barv + 16u * C::kVStages;
+  auto s_full = [&](int x) { return barx + 8u * x; };
+  auto p_full = [&](int x) { return barx + 16u + 8u * x; };
+  auto pv_done = [&](int x) { return barx + 32u + 8u * x; };
+  auto o_free = [&](int x) { return barx + 48u + 8u * x; };
+  const uint32_t drain_bar = barx + 64u;
+  auto seg_full = [&](uint32_t i) { return barx + 72u + 8u * (i % C::kRing); };
+  auto seg_empty = [&](uint32_t i) { return barx + 72u + 8u * (C::kRing + i % C::kRing); };
+  int4* ring = reinterpret_cast<int4*>(smem + C::kOffRing);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffRing + 32 * C::kRing);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  unsigned int* err = &g_mtp_error_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kQTiles; ++i) {
+      mbar_init(q_full(i), 32);
+      mbar_init(q_empty(i), 1);
+    }
+    for (int i = 0; i < C::kKStages; ++i) {
+      mbar_init(k_full(i), 1);
+      mbar_init(k_empty(i), 1);
+    }
+    for (int i = 0; i < C::kVStages; ++i) {
+      mbar_init(v_full(i), 1);
+      mbar_init(v_empty(i), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(s_full(x), 1);
+      mbar_init(p_full(x), kRows);
+      mbar_init(pv_done(x), 1);
+      mbar_init(o_free(x), kRows);
+    }
+    mbar_init(drain_bar, 1);
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(seg_full(i), 1);
+      mbar_init(seg_empty(i), C::kReaders);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == C::kMmaWarp) tmem_alloc_cols(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, err); };
+  // segment i, read by one thread
+  auto peek_segment = [&](uint32_t i, Segment& s) {
+    if (!wait(seg_full(i), (i / C::kRing) & 1)) return false;
+    const int4 a = ring[2 * (i % C::kRing)], b = ring[2 * (i % C::kRing) + 1];
+    s = Segment{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return s.kind >= 0;
+  };
+  auto read_segment = [&](uint32_t i, Segment& s) {
+    if (!peek_segment(i, s)) return false;
+    mbar_arrive1(seg_empty(i));
+    return true;
+  };
+  // ... by a warp: its slot is released once every lane has read it
+  auto read_segment_warp = [&](uint32_t i, Segment& s) {
+    if (!__all_sync(0xffffffffu, peek_segment(i, s))) return false;
+    if (lane == 0) mbar_arrive1(seg_empty(i));
+    return true;
+  };
+  auto first_row = [&](const Segment& s) { return s.tile * 2 * kRows; };
+
+  if (warp == C::kTmaWarp) {
+    // ---------------- TMA producers: lane 0 the deal and K, lane 1 V ----------------
+    // blocks of all own caches, then the request that this CTA's range starts in
+    long long own = 0;
+    for (int r = lane; r < sh.R; r += 32) own += sh.blocks_of(sh.ctx(r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    const Deal deal(sh, own);
+    const int cta = static_cast<int>(blockIdx.x);
+    const long long prefix_total = sh.prefix_total(), step = sh.own_step();
+    long long pos = cta < deal.n ? deal.start(cta) : 0;
+    const long long end = cta < deal.n ? deal.start(cta + 1) : 0;
+    int r0 = 0;
+    long long before = 0;  // own blocks of the requests before r0
+    if (end > pos && end > prefix_total) {
+      const long long want = pos > prefix_total ? (pos - prefix_total) / step : 0;  // a block, over all requests
+      for (int base = 0; base < sh.R; base += 32) {
+        const int nb = base + lane < sh.R ? sh.blocks_of(sh.ctx(base + lane)) : 0;
+        int incl = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, before + incl > want);
+        if (over) {
+          const int src = __ffs(over) - 1;
+          r0 = base + src;
+          before += __shfl_sync(0xffffffffu, incl - nb, src);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+    }
+    if (lane < 2) {
+      const bool kside = lane == 0;
+      const uint32_t stages = kside ? C::kKStages : C::kVStages;
+      uint32_t g = 0;
+      bool ok = true;
+      auto load = [&](const Segment& s) {  // the segment's blocks
+        for (int j = 0; j < s.n; ++j, ++g) {
+          const uint32_t use = g / stages;
+          if (use > 0 && !wait(kside ? k_empty(g) : v_empty(g), (use - 1) & 1)) { ok = false; return; }
+          const int key = (s.b0 + j) * kKeys;
+          if (kside) {
+            const CUtensorMap* m = s.kind & 1 ? &kk : &pk;
+            mbar_expect_tx(k_full(g), C::kTileBytes);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_tile_4d(sK + (g % C::kKStages) * C::kTileBytes + c * C::kPiece, m, 64 * c, s.head, key, s.r, k_full(g));
+          } else {
+            const CUtensorMap* m = s.kind & 1 ? &kv : &pv;
+            mbar_expect_tx(v_full(g), C::kTileBytes);
+            for (int half = 0; half < 2; ++half)
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_tile_4d(sV + (g % C::kVStages) * C::kTileBytes + (half * C::kChunks + c) * 8192, m, 64 * c, s.head,
+                            key + 64 * half, s.r, v_full(g));
+          }
+        }
+      };
+      if (kside) {
+        uint32_t i = 0;
+        auto publish = [&](const Segment& s) {
+          if (i >= static_cast<uint32_t>(C::kRing) && !wait(seg_empty(i), (i / C::kRing - 1) & 1)) { ok = false; return; }
+          ring[2 * (i % C::kRing)] = make_int4(s.kind, s.head, s.tile, s.r);
+          ring[2 * (i % C::kRing) + 1] = make_int4(s.b0, s.n, s.keys, s.rec);
+          mbar_arrive1(seg_full(i));
+          ++i;
+          if (s.kind >= 0) load(s);
+        };
+        // blocks of the item that starts at `at` which start in [pos, end)
+        auto cut = [&](long long at, int blocks, int cost, Segment& s) {
+          const long long lo = pos > at ? (pos - at + cost - 1) / cost : 0;
+          const long long hi = end > at ? (end - at + cost - 1) / cost : 0;
+          s.b0 = static_cast<int>(min(lo, static_cast<long long>(blocks)));
+          s.n = static_cast<int>(min(hi, static_cast<long long>(blocks))) - s.b0;
+          return s.n > 0;
+        };
+        if (pos < prefix_total) {
+          const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
+          for (int item = static_cast<int>(pos / cost); ok && item < sh.Hkv * sh.prefix_tiles && item * cost < end; ++item) {
+            Segment s;
+            s.head = item / sh.prefix_tiles;
+            s.tile = item - s.head * sh.prefix_tiles;
+            s.kind = sh.prefix_rows - first_row(s) > kRows ? 2 : 0;
+            s.r = 0;
+            s.keys = sh.P;
+            s.rec = item + cta;
+            if (cut(item * cost, sh.prefix_blocks, sh.prefix_cost, s)) publish(s);
+          }
+        }
+        const int per_r = sh.Hkv * sh.own_tiles;
+        for (int r = r0; ok && end > prefix_total && r < sh.R; ++r) {
+          const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
+          const long long at0 = prefix_total + before * step, cost = static_cast<long long>(nb) * sh.own_cost;
+          if (at0 >= end) break;
+          before += nb;
+          if (nb == 0) continue;
+          for (int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0; ok && h < per_r && at0 + h * cost < end; ++h) {
+            Segment s;
+            s.head = h / sh.own_tiles;
+            s.tile = h - s.head * sh.own_tiles;
+            s.kind = 1 | (sh.own_rows - first_row(s) > kRows ? 2 : 0);
+            s.r = r;
+            s.keys = keys;
+            s.rec = r * per_r + h + cta;
+            if (cut(at0 + h * cost, nb, sh.own_cost, s)) publish(s);
+          }
+        }
+        Segment last{};
+        last.kind = -1;
+        if (ok) publish(last);
+      } else {
+        Segment s;
+        for (uint32_t i = 0; ok && read_segment(i, s); ++i) load(s);
+      }
+      // no copy may still be landing when the CTA leaves (matters only after an abort)
+      for (uint32_t x = g > stages ? g - stages : 0; x < g; ++x)
+        wait_drain(kside ? k_full(x) : v_full(x), (x / stages) & 1, kWaitLimitCycles);
+    }
+  } else if (warp == C::kQWarp) {
+    // ---------------- Q: rows gathered into the 128-byte swizzled layout ----------------
+    Segment s;
+    uint32_t tile = 0;
+    bool ok = true;
+    for (uint32_t i = 0; ok && read_segment_warp(i, s); ++i) {
+      const int n_tiles = s.kind & 2 ? 2 : 1, rows = s.kind & 1 ? sh.own_rows : sh.prefix_rows;
+      for (int x = 0; ok && x < n_tiles; ++x, ++tile) {
+        const uint32_t use = tile / C::kQTiles;
+        if (use > 0 && !__all_sync(0xffffffffu, wait(q_empty(tile), (use - 1) & 1))) { ok = false; break; }
+        const uint32_t dst = sQ + (tile % C::kQTiles) * C::kTileBytes;
+        // 16-byte pieces: HD / 8 lanes per row
+        constexpr int kPer = HD / 8, kStep = 32 / kPer;
+        const int piece = lane % kPer;
+        for (int row = lane / kPer; row < kRows; row += kStep) {
+          const int rho = first_row(s) + x * kRows + row;
+          const bool live = rho < rows;
+          const int token = live ? rho / sh.G : 0, hg = live ? rho - token * sh.G : 0;
+          const int rr = s.kind & 1 ? s.r : token / sh.L, ll = s.kind & 1 ? token : token - rr * sh.L;
+          const __nv_bfloat16* src = q + rr * q_r + ll * q_l + (s.head * sh.G + hg) * q_h + piece * 8;
+          const uint32_t at = dst + (piece >> 3) * C::kPiece + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(live ? 16 : 0) : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive1(q_full(tile));
+      }
+    }
+  } else if (warp == C::kMmaWarp) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
+      uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
+      uint32_t ns[2] = {0u, 0u};    // S products issued per TMEM tile
+      uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose output has been read
+      bool ok = true, any = false;
+      Segment s;
+      for (uint32_t i = 0; ok && read_segment(i, s); ++i) {
+        const bool two = s.kind & 2;
+        const int n = s.n;
+        bool first_pv[2] = {true, true};
+        for (int x = 0; ok && x < (two ? 2 : 1); ++x)
+          if (!wait(q_full(tile + x), ((tile + x) / C::kQTiles) & 1)) ok = false;
+        if (!ok) break;
+        tc_fence_after();
+        // S_x = Q K^T of ring block gu; the P that shared its columns was read by a product issued before
+        auto issue_s = [&](int x, uint32_t gu) {
+          const uint32_t q_at = sQ + ((tile + (two ? x : 0)) % C::kQTiles) * C::kTileBytes;
+          const uint32_t k_at = sK + (gu % C::kKStages) * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t off = (k >> 2) * C::kPiece + (k & 3) * 32;
+            umma_bf16_ss(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
+          }
+          umma_commit(s_full(x));
+          ++ns[x];
+          any = true;
+        };
+        auto wait_k = [&](uint32_t gu) {
+          if (!wait(k_full(gu), (gu / C::kKStages) & 1)) return false;
+          tc_fence_after();
+          return true;
+        };
+        // O_x (+)= P_x V of ring block gu
+        auto issue_pv = [&](int x, uint32_t gu) {
+          if (!wait(p_full(x), (ns[x] - 1) & 1)) return false;
+          if (first_pv[x] && no[x] > 0 && !wait(o_free(x), (no[x] - 1) & 1)) return false;
+          tc_fence_after();
+          const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k) {
+            const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
+            umma_bf16_ts(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
+                         (!first_pv[x] || k > 0) ? 1u : 0u);
+          }
+          umma_commit(pv_done(x));
+          first_pv[x] = false;
+          return true;
+        };
+        auto release_q = [&]() {
+          umma_commit(q_empty(tile));
+          if (two) umma_commit(q_empty(tile + 1));
+        };
+        if (two) {
+          if (!wait_k(g)) { ok = false; break; }
+          issue_s(0, g);
+          issue_s(1, g);
+          umma_commit(k_empty(g));
+          if (n == 1) release_q();
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t gu = g + j;
+            if (!wait(v_full(gu), (gu / C::kVStages) & 1)) { ok = false; break; }
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (!issue_pv(x, gu)) { ok = false; break; }
+              if (j + 1 < n) {
+                if (x == 0 && !wait_k(gu + 1)) { ok = false; break; }
+                issue_s(x, gu + 1);
+              }
+            }
+            if (!ok) break;
+            umma_commit(v_empty(gu));
+            if (j + 1 < n) umma_commit(k_empty(gu + 1));
+            if (j + 2 == n) release_q();
+          }
+        } else {
+          for (int j = 0; j < min(n, 2) && ok; ++j) {
+            if (!wait_k(g + j)) { ok = false; break; }
+            issue_s(j, g + j);
+            umma_commit(k_empty(g + j));
+          }
+          if (!ok) break;
+          if (n <= 2) release_q();
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t gu = g + j;
+            if (!wait(v_full(gu), (gu / C::kVStages) & 1) || !issue_pv(j & 1, gu)) { ok = false; break; }
+            umma_commit(v_empty(gu));
+            if (j + 2 < n) {
+              if (!wait_k(gu + 2)) { ok = false; break; }
+              issue_s(j & 1, gu + 2);
+              umma_commit(k_empty(gu + 2));
+              if (j + 3 == n) release_q();
+            }
+          }
+        }
+        g += n;
+        tile += two ? 2 : 1;
+        ++no[0];
+        if (two || n > 1) ++no[1];
+      }
+      // every issued MMA has completed before TMEM is freed
+      if (any) {
+        umma_commit(drain_bar);
+        wait_drain(drain_bar, 0, kWaitLimitCycles);
+      }
+    }
+  } else {
+    // ---------------- softmax: one row per thread of tile x ----------------
+    const int x = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t colS = 128u * x, colO = C::kColO + HD * x;
+    auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    uint32_t n = 0;  // S products of this tile consumed
+    uint32_t g = 0;  // key blocks of the CTA's earlier segments
+    Segment s;
+    for (uint32_t i = 0; read_segment_warp(i, s); ++i) {
+      const bool two = s.kind & 2, own = s.kind & 1;
+      const int rows = own ? sh.own_rows : sh.prefix_rows;
+      const int rho = first_row(s) + (two ? x * kRows : 0) + row;
+      const bool live = rho < rows;
+      const bool live_warp = first_row(s) + (two ? x * kRows : 0) + (warp & 3) * 32 < rows;
+      // keys that the row sees
+      int see = s.keys;
+      if (own && sh.causal) see = max(0, s.keys - sh.L + 1 + rho / sh.G);
+      const int mine = two ? s.n : (s.n + 1 - x) >> 1;  // blocks of this tile
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < mine; ++j, ++n) {
+        if (!wwait(s_full(x), n & 1)) { ok = false; break; }
+        tc_fence_after();
+        const int jb = two ? j : 2 * j + x;
+        const int key0 = (s.b0 + jb) * kKeys;
+        if (own && s.keys - key0 < kKeys && (!two || x == 0)) {  // V rows past the end of the request's cache
+          const uint32_t gu = g + jb;
+          if (!wwait(v_full(gu), (gu / C::kVStages) & 1)) { ok = false; break; }
+          if (row >= s.keys - key0) {
+            uint8_t* v = smem + C::kOffV + (gu % C::kVStages) * C::kTileBytes + (row >> 6) * (C::kChunks * 8192) + (row & 63) * 128;
+            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) reinterpret_cast<uint4*>(v + c * 8192)[e] = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (live_warp) {
+          float sc[128];
+          {
+            float (&lo)[64] = *reinterpret_cast<float (*)[64]>(&sc[0]);
+            float (&hi)[64] = *reinterpret_cast<float (*)[64]>(&sc[64]);
+            tmem_ld64(lane_base + colS, lo);
+            tmem_ld64(lane_base + colS + 64, hi);
+          }
+          if (see - key0 < kKeys) {  // keys the row sees only in part
+#pragma unroll
+            for (int e = 0; e < 128; ++e)
+              if (key0 + e >= see) sc[e] = -INFINITY;
+          }
+          float mx8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx8[e] = sc[e];
+#pragma unroll
+          for (int e = 8; e < 128; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], sc[e]);
+          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scale_log2;
+          // a new running maximum only when the block's exceeds the stale one by 2^8
+          const float m_new = mx > m + kStaleMaxLog2 ? mx : m;
+          const bool rescale = m_new != m && m != -INFINITY;
+          const float neg = m_new == -INFINITY ? 0.f : -m_new;
+          float rs8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rs8[e] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) {  // P pairs packed in place: sc[e] holds keys 2e, 2e+1
+            const float a = ex2(fmaf(sc[2 * e], scale_log2, neg));
+            const float b = ex2(fmaf(sc[2 * e + 1], scale_log2, neg));
+            rs8[e & 7] += a + b;
+            sc[e] = __uint_as_float(pack2_bf16(a, b));
+          }
+          if (__any_sync(0xffffffffu, rescale)) {  // O holds this segment's earlier P V: wait for the last one
+            if (!wwait(pv_done(x), (n - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            const float alpha = rescale ? ex2(m - m_new) : 1.f;
+#pragma unroll
+            for (int c = 0; c < HD / 32; ++c) {
+              float o[32];
+              tmem_ld32(lane_base + colO + 32 * c, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32(lane_base + colO + 32 * c, o);
+            }
+            l *= alpha;
+          }
+          m = m_new;
+          l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float (&p)[32] = *reinterpret_cast<float (*)[32]>(&sc[32 * c]);
+            tmem_st32(lane_base + colS + 32 * c, p);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive1(p_full(x));
+      }
+      if (!ok) break;
+      g += s.n;
+      // the segment's record of this row (of this tile's half of them with one row tile)
+      const int rec_rows = own ? sh.own_rec : sh.prefix_rec;
+      const long long at = (own ? sh.own_rec0 : 0) + static_cast<long long>(s.rec) * rec_rows + x * (rec_rows / 2) + row;
+      if (mine > 0) {
+        if (!wwait(pv_done(x), (n - 1) & 1)) break;  // the segment's last P V
+        tc_fence_after();
+        if (live_warp) {
+#pragma unroll
+          for (int c = 0; c < HD / 32; ++c) {
+            float o[32];
+            tmem_ld32(lane_base + colO + 32 * c, o);
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(rec_o + at * HD + 32 * c);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) dst[v] = make_float4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive1(o_free(x));
+      }
+      if (live) rec_ml[at] = make_float2(m, l);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::kMmaWarp) tmem_free_cols(tmem, 512);
+}
+
+// Joins the records of one (request, token, head) per warp: lanes over the
+// records for the maximum and the weights, then over the head's dimensions.
+template <int HD>
+__global__ void __launch_bounds__(256)
+prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const float* __restrict__ rec_o,
+                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
+  __shared__ int s_sum[8], s_before[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y;
+  // own blocks of all requests, and of those before r
+  int sum = 0, before = 0;
+  for (int i = threadIdx.x; i < sh.R; i += 256) {
+    const int nb = sh.blocks_of(sh.ctx(i));
+    sum += nb;
+    if (i < r) before += nb;
+  }
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (lane == 0) {
+    s_sum[warp] = sum;
+    s_before[warp] = before;
+  }
+  __syncthreads();
+  long long all = 0, prev = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    all += s_sum[w];
+    prev += s_before[w];
+  }
+  pdl_wait();  // the records are the previous kernel's
+  const int item = blockIdx.x * 8 + warp;
+  if (item >= sh.L * sh.H) return;
+  const int i = item / sh.H, h = item - i * sh.H, head = h / sh.G, hg = h - head * sh.G;
+  const Deal deal(sh, all);
+  // record rows: `n` segments from record row `at` on, `rows` apart, each with `halves` parts rows / 2 apart
+  struct Run {
+    long long at;
+    int n, rows, halves;
+  } run[2];
+  {
+    const int rho = (r * sh.L + i) * sh.G + hg, tile = rho / (2 * kRows), in = rho - tile * 2 * kRows;
+    const bool two = sh.prefix_rows - tile * 2 * kRows > kRows;
+    const int k = head * sh.prefix_tiles + tile;
+    const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost, at = k * cost;
+    run[0] = Run{0, 0, sh.prefix_rec, two ? 1 : 2};
+    if (cost > 0) {
+      const int a = deal.owner(at), b = deal.owner(at + cost - sh.prefix_cost);
+      run[0].n = b - a + 1;
+      run[0].at = static_cast<long long>(k + a) * sh.prefix_rec + in;
+    }
+  }
+  {
+    const int rho = i * sh.G + hg, tile = rho / (2 * kRows), in = rho - tile * 2 * kRows;
+    const bool two = sh.own_rows - tile * 2 * kRows > kRows;
+    const int nb = sh.blocks_of(sh.ctx(r)), k = head * sh.own_tiles + tile;
+    const long long cost = static_cast<long long>(nb) * sh.own_cost;
+    const long long at = sh.prefix_total() + prev * sh.own_step() + k * cost;
+    run[1] = Run{0, 0, sh.own_rec, two ? 1 : 2};
+    if (nb > 0) {
+      const int a = deal.owner(at), b = deal.owner(at + cost - sh.own_cost);
+      run[1].n = b - a + 1;
+      run[1].at = sh.own_rec0 + static_cast<long long>(r * sh.Hkv * sh.own_tiles + k + a) * sh.own_rec + in;
+    }
+  }
+  const int n0 = run[0].n * run[0].halves, parts = n0 + run[1].n * run[1].halves;
+  auto part_at = [&](int p) {
+    const Run& u = run[p < n0 ? 0 : 1];
+    const int e = p < n0 ? p : p - n0, seg = e / u.halves, half = e - seg * u.halves;
+    return u.at + static_cast<long long>(seg) * u.rows + half * (u.rows / 2);
+  };
+  float M = -INFINITY;
+  for (int p = lane; p < parts; p += 32) {
+    const float2 ml = rec_ml[part_at(p)];
+    if (ml.y > 0.f || ml.y != ml.y) M = fmaxf(M, ml.x);
+  }
+  M = warp_max(M);
+  const float Ms = M == -INFINITY ? 0.f : M;
+  constexpr int kD = HD / 32;
+  float acc[kD], L = 0.f;
+#pragma unroll
+  for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += 32) {
+    long long at = 0;
+    float w = 0.f;
+    if (p0 + lane < parts) {
+      at = part_at(p0 + lane);
+      const float2 ml = rec_ml[at];
+      if (ml.y > 0.f || ml.y != ml.y) {
+        w = ex2(ml.x - Ms);
+        L += w * ml.y;
+      }
+    }
+    const int n = min(32, parts - p0);
+#pragma unroll 4
+    for (int e = 0; e < n; ++e) {
+      const float we = __shfl_sync(0xffffffffu, w, e);
+      const long long ae = __shfl_sync(0xffffffffu, at, e);
+      if (we != 0.f) {  // warp-uniform (NaN too); a part without a key has no output to read
+        const float* src = rec_o + ae * HD + lane * kD;
+        if constexpr (kD == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          acc[0] = fmaf(we, v.x, acc[0]);
+          acc[1] = fmaf(we, v.y, acc[1]);
+          acc[2] = fmaf(we, v.z, acc[2]);
+          acc[3] = fmaf(we, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          acc[0] = fmaf(we, v.x, acc[0]);
+          acc[1] = fmaf(we, v.y, acc[1]);
+        }
+      }
+    }
+  }
+  L = warp_sum(L);
+  const long long out = (static_cast<long long>(r) * sh.L + i) * sh.H + h;
+  if (rec) {
+    float* to = rec + out * rec_stride;
+    if (lane == 0) {
+      to[0] = M * kLn2;
+      to[1] = L;
+    }
+#pragma unroll
+    for (int d = 0; d < kD; ++d) to[2 + lane * kD + d] = acc[d];
+    return;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees no key: zeros
+  __nv_bfloat16* to = o + out * HD + lane * kD;
+  if constexpr (kD == 4)
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(to) = pack2_bf16(acc[0] * inv, acc[1] * inv);
+  if (lse && lane == 0) lse[out] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+}
+
+inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+Shape make_shape(int R, int L, int H, int Hkv, int hd, int P, int T) {
+  Shape s{};
+  s.R = R;
+  s.L = L;
+  s.H = H;
+  s.Hkv = Hkv;
+  s.G = H / Hkv;
+  s.hd = hd;
+  s.P = P;
+  s.T = T;
+  s.prefix_rows = R * L * s.G;
+  s.own_rows = L * s.G;
+  s.prefix_tiles = (s.prefix_rows + 2 * kRows - 1) / (2 * kRows);
+  s.own_tiles = (s.own_rows + 2 * kRows - 1) / (2 * kRows);
+  s.prefix_blocks = (P + kKeys - 1) / kKeys;
+  s.prefix_cost = s.prefix_rows > kRows ? kCostTwo : kCostOne;
+  s.own_cost = s.own_rows > kRows ? kCostTwo : kCostOne;
+  s.prefix_rec = s.prefix_rows > kRows ? 2 * kRows : 2 * s.prefix_rows;
+  s.own_rec = s.own_rows > kRows ? 2 * kRows : 2 * s.own_rows;
+  s.grid = sm_count_current();
+  s.own_rec0 = P > 0 ? (static_cast<long long>(Hkv) * s.prefix_tiles + s.grid) * s.prefix_rec : 0;
+  return s;
+}
+long long record_rows(const Shape& s) {
+  return s.own_rec0 + (s.T > 0 ? (static_cast<long long>(s.R) * s.Hkv * s.own_tiles + s.grid) * s.own_rec : 0);
+}
+
+// keys or values as (dimension, head, token, request); boxes of 64 dimensions x `box` tokens of one head
+bool kv_map(CUtensorMap* m, const void* p, int hd, int heads, int tokens, int requests, long long s_h, long long s_t,
+            long long s_r, int box) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens),
+                            static_cast<uint64_t>(requests)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(s_h) * 2, static_cast<uint64_t>(s_t) * 2, static_cast<uint64_t>(s_r) * 2};
+  const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
+  return tensor_map_bf16_4d(m, p, dims, strides, boxes);
+}
+
+template <int HD>
+mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cudaStream_t st) {
+  using C = Cfg<HD>;
+  static PerDevice attr;
+  if (!smem_limit(attr, prefix_attn_kernel<HD>, C::kSmemBytes)) return MTP_ERR_CUDA;
+  CUtensorMap pk{}, pv{}, kk{}, kv{};
+  if (p.P > 0 && (!kv_map(&pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, kKeys) ||
+                  !kv_map(&pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 64)))
+    return MTP_ERR_CUDA;
+  if (p.T > 0 && (!kv_map(&kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, kKeys) ||
+                  !kv_map(&kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 64)))
+    return MTP_ERR_CUDA;
+  const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
+  if (p.P > 0 || p.T > 0) {
+    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(pk, pv, kk, kv, s, p.q, p.q_r, p.q_l, p.q_h,
+                                                                      scale * kLog2e, ml, ro);
+    note_launch();
+    MTP_LAUNCH_CHECK();
+  }
+  const dim3 grid((s.L * s.H + 7) / 8, s.R);
+  if (p.P > 0 || p.T > 0)
+    MTP_CUDA_TRY(launch_pdl(prefix_join_kernel<HD>, grid, dim3(256), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
+  else
+    prefix_join_kernel<HD><<<grid, 256, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
+  note_launch();
+  MTP_LAUNCH_CHECK();
+  return MTP_OK;
+}
+
+bool sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T) {
+  return R >= 1 && R <= 65535 && L >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && (hd == 64 || hd == 128) && P >= 0 && T >= 0 &&
+         static_cast<long long>(R) * L * H <= (1 << 24) && static_cast<long long>(P) + T <= 0x7FFFFF00ll;
+}
+
+}  // namespace
+
+size_t prefix_attn_workspace_bytes(int R, int L, int H, int Hkv, int hd, int P, int T) {
+  if (!sizes_ok(R, L, H, Hkv, hd, P, T)) return 0;
+  const long long rows = record_rows(make_shape(R, L, H, Hkv, hd, P, T));
+  return up256(rows * sizeof(float2)) + up256(static_cast<size_t>(rows) * hd * 4) + 256;
+}
+
+mtp_status prefix_attn_launch(const PrefixAttn& p, void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!sizes_ok(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_SHAPE;
+  if (ws_bytes < prefix_attn_workspace_bytes(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_WORKSPACE;
+  Shape s = make_shape(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T);
+  s.causal = p.causal;
+  s.ctx_len = p.ctx_len;
+  float2* ml = static_cast<float2*>(ws);
+  float* ro = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + up256(record_rows(s) * sizeof(float2)));
+  return p.hd == 64 ? launch<64>(p, s, ml, ro, st) : launch<128>(p, s, ml, ro, st);
+}
+
+}  // namespace mtp
+
+extern "C" size_t mtp_prefix_attention_workspace_bytes(const mtp_prefix_dims* d) {
+  return d ? mtp::prefix_attn_workspace_bytes(d->R, d->L, d->n_heads, d->n_kv_heads, d->head_dim, d->P, d->T) : 0;
+}
+
+extern "C" mtp_status mtp_prefix_attention(const mtp_prefix_dims* d, const void* q, const void* prefix_k, const void* prefix_v,
+                                           const void* kv_k, const void* kv_v, const int32_t* ctx_len, void* out, float* lse,
+                                           void* ws, size_t ws_bytes, cudaStream_t st) {
+  if (!d) return MTP_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return MTP_ERR_UNSUPPORTED;
+  if (!mtp::sizes_ok(d->R, d->L, d->n_heads, d->n_kv_heads, d->head_dim, d->P, d->T)) return MTP_ERR_SHAPE;
+  if (!(d->scale >= 0.f) || d->scale > 3.0e38f) return MTP_ERR_INVALID_ARG;
+  if (!q || !out || !ws || (d->P > 0 && (!prefix_k || !prefix_v)) || (d->T > 0 && (!kv_k || !kv_v))) return MTP_ERR_INVALID_ARG;
+  const long long hd = d->head_dim, row = hd * d->n_kv_heads, q_row = hd * d->n_heads;
+  mtp::PrefixAttn p;
+  p.R = d->R;
+  p.L = d->L;
+  p.H = d->n_heads;
+  p.Hkv = d->n_kv_heads;
+  p.hd = d->head_dim;
+  p.P = d->P;
+  p.T = d->T;
+  p.causal = d->causal != 0;
+  p.scale = d->scale;
+  p.q_h = d->q_stride_h ? d->q_stride_h : hd;
+  p.q_l = d->q_stride_t ? d->q_stride_t : q_row;
+  p.q_r = d->q_stride_r ? d->q_stride_r : q_row * d->L;
+  p.p_h = d->prefix_stride_h ? d->prefix_stride_h : hd;
+  p.p_t = d->prefix_stride_t ? d->prefix_stride_t : row;
+  p.k_h = d->kv_stride_h ? d->kv_stride_h : hd;
+  p.k_t = d->kv_stride_t ? d->kv_stride_t : row;
+  p.k_r = d->kv_stride_r ? d->kv_stride_r : row * std::max(d->T, 1);
+  for (long long s : {p.q_h, p.q_l, p.q_r, p.p_h, p.p_t, p.k_h, p.k_t, p.k_r}) {
+    if (s < 0 || s >= (1ll << 38)) return MTP_ERR_SHAPE;
+    if (s % 8) return MTP_ERR_ALIGNMENT;  // 16-byte copies
+  }
+  for (const void* a : {q, prefix_k, prefix_v, kv_k, kv_v, static_cast<const void*>(out), static_cast<const void*>(ws)})
+    if (!mtp::aligned16(a)) return MTP_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(ctx_len) & 3u)) return MTP_ERR_ALIGNMENT;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.pk = static_cast<const __nv_bfloat16*>(prefix_k);
+  p.pv = static_cast<const __nv_bfloat16*>(prefix_v);
+  p.kk = static_cast<const __nv_bfloat16*>(kv_k);
+  p.kv = static_cast<const __nv_bfloat16*>(kv_v);
+  p.ctx_len = ctx_len;
+  p.o = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  return mtp::prefix_attn_launch(p, ws, ws_bytes, st);
+}

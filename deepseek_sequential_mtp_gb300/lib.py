@@ -64,6 +64,13 @@ class Int4Matrix(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
 
 
+class PrefixDims(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int) for k in ("R", "L", "n_heads", "n_kv_heads", "head_dim", "P", "T", "causal")] + \
+               [("scale", ctypes.c_float)] + \
+               [(k, ctypes.c_longlong) for k in ("q_stride_r", "q_stride_t", "q_stride_h", "prefix_stride_t",
+                                                 "prefix_stride_h", "kv_stride_r", "kv_stride_t", "kv_stride_h")]
+
+
 class LogitsParams(ctypes.Structure):
     _fields_ = [(k, ctypes.c_void_p) for k in ("temperature", "repetition", "frequency", "presence", "hist",
                                                "hist_len", "prompt_len", "draft", "bias_ids", "bias", "mask")] + \
@@ -140,6 +147,10 @@ def load() -> ctypes.CDLL:
                                             ctypes.c_longlong, vp]
     lib.mtp_gemm_int4w.restype = i32
     lib.mtp_gemm_int4w.argtypes = [i32, i32, i32, i32, vp, ctypes.POINTER(Int4Matrix), vp, i32, vp]
+    lib.mtp_prefix_attention_workspace_bytes.restype = sz
+    lib.mtp_prefix_attention_workspace_bytes.argtypes = [ctypes.POINTER(PrefixDims)]
+    lib.mtp_prefix_attention.restype = i32
+    lib.mtp_prefix_attention.argtypes = [ctypes.POINTER(PrefixDims)] + [vp] * 9 + [sz, vp]
     lib.mtp_logits_probs.restype = i32
     lib.mtp_logits_probs.argtypes = [i32, i32, i32, i32, vp, ctypes.c_longlong, ctypes.POINTER(LogitsParams), vp, vp,
                                      vp]
@@ -730,3 +741,76 @@ class DraftRound:
         if h_out is not None:
             out["h"] = h_out
         return out
+
+
+# --------------------------------------------------------------------------
+# Attention over a shared prefix
+# --------------------------------------------------------------------------
+def _strides(t: torch.Tensor, name: str):
+    """Strides of all dimensions but the last, which has to be dense; 0 (of no
+    consequence) for those of one element."""
+    if t.numel() == 0:
+        return [0] * (t.dim() - 1)
+    if t.stride(-1) != 1:
+        raise MtpError(f"{name} must be dense in its last dimension")
+    if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise MtpError(f"{name} must not be expanded")
+    return [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+
+
+def _pair(k, v, name: str, dims: int, device):
+    """Keys and values of one shape and layout, the last dimension dense."""
+    for n, t in ((name + "_k", k), (name + "_v", v)):
+        if t.dim() != dims or t.dtype != torch.bfloat16 or t.device != device:
+            raise MtpError(f"{n} must be a bfloat16 tensor of {dims} dimensions on {device}")
+    if k.shape != v.shape or _strides(k, name + "_k") != _strides(v, name + "_v"):
+        raise MtpError(f"{name}_k and {name}_v must have the same shape and strides")
+
+
+def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor,
+                     kv_k: Optional[torch.Tensor] = None, kv_v: Optional[torch.Tensor] = None,
+                     ctx_len: Optional[torch.Tensor] = None, causal: bool = True, scale: Optional[float] = None,
+                     out: Optional[dict] = None, ws: Optional[torch.Tensor] = None, stream=None) -> dict:
+    """Attention of q [R, L, H, hd] over a prefix [P, Hkv, hd] that all requests
+    share and each request's own cache [R, T, Hkv, hd] of ctx_len[r] rows, the
+    last L of them the new tokens' own (include/mtp.h: mtp_prefix_attention).
+    Any strides that are multiples of 8 with a dense last dimension will do.
+    Returns {"o": bfloat16 [R, L, H, hd], "lse": float32 [R, L, H]}; ``out`` may
+    supply them."""
+    if q.dim() != 4 or q.dtype != torch.bfloat16:
+        raise MtpError("q must be bfloat16 [R, L, H, hd]")
+    dev = _launch_device(q, stream)
+    R, L, H, hd = q.shape
+    _pair(prefix_k, prefix_v, "prefix", 3, dev)
+    P, Hkv = prefix_k.shape[0], prefix_k.shape[1]
+    if prefix_k.shape[2] != hd:
+        raise MtpError("prefix_k must be [P, Hkv, hd]")
+    d = PrefixDims(R, L, H, Hkv, hd, P, 0, int(causal), 0.0 if scale is None else float(scale))
+    if scale is not None and not 0.0 < scale < 3e38:
+        raise MtpError("scale must be positive and finite")
+    d.q_stride_r, d.q_stride_t, d.q_stride_h = _strides(q, "q")
+    d.prefix_stride_t, d.prefix_stride_h = _strides(prefix_k, "prefix_k")
+    if (kv_k is None) != (kv_v is None):
+        raise MtpError("kv_k and kv_v come together")
+    if kv_k is not None:
+        _pair(kv_k, kv_v, "kv", 4, dev)
+        if kv_k.shape[0] != R or tuple(kv_k.shape[2:]) != (Hkv, hd):
+            raise MtpError("kv_k must be [R, T, Hkv, hd]")
+        d.T = kv_k.shape[1]
+        d.kv_stride_r, d.kv_stride_t, d.kv_stride_h = _strides(kv_k, "kv_k")
+    elif ctx_len is not None:
+        raise MtpError("ctx_len needs kv_k and kv_v")
+    ctx = _arg(ctx_len, "ctx_len", torch.int32, (R,), dev)
+    if out is None:
+        out = {"o": _empty((R, L, H, hd), torch.bfloat16, dev, stream), "lse": _empty((R, L, H), torch.float32, dev, stream)}
+    else:
+        _arg(out["o"], "out['o']", torch.bfloat16, (R, L, H, hd), dev)
+        _arg(out["lse"], "out['lse']", torch.float32, (R, L, H), dev)
+    lib = load()
+    if ws is None:
+        ws = _empty(int(lib.mtp_prefix_attention_workspace_bytes(ctypes.byref(d))), torch.uint8, dev, stream)
+    st = lib.mtp_prefix_attention(ctypes.byref(d), q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(),
+                                  kv_k.data_ptr() if d.T > 0 else None, kv_v.data_ptr() if d.T > 0 else None, ctx,
+                                  out["o"].data_ptr(), out["lse"].data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    _check(st, "mtp_prefix_attention")
+    return out

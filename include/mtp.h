@@ -109,7 +109,8 @@ enum {
   MTP_DEVERR_FROM_VERIFY = 1u << 11, /* spec_verify                               */
   MTP_DEVERR_FROM_DRAFT = 1u << 12,  /* draft-step kernels                        */
   MTP_DEVERR_FROM_FP8 = 1u << 13,    /* FP8 block-scaled weight GEMM              */
-  MTP_DEVERR_FROM_DGEMM = 1u << 14   /* bf16 decode-shaped GEMM                   */
+  MTP_DEVERR_FROM_DGEMM = 1u << 14,  /* bf16 decode-shaped GEMM                   */
+  MTP_DEVERR_FROM_PREFIX = 1u << 15  /* shared-prefix attention                    */
 };
 
 /* Problem sizes of one chain call.
@@ -408,6 +409,49 @@ mtp_status mtp_draft_round(const mtp_dims* dims, const mtp_weights* w, const voi
                            const int32_t* frontier, const int32_t* pos, const void* kv_k, const void* kv_v,
                            const int32_t* ctx_len, int gamma, uint64_t seed, uint64_t offset, float* q_out,
                            int32_t* y_out, void* h_out, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Sizes and layouts of mtp_prefix_attention: R requests with L new tokens each,
+ * n_heads query heads of which n_heads / n_kv_heads consecutive ones share a
+ * key head, head_dim 64 or 128, P rows of shared prefix (0: none), T rows of
+ * capacity in each request's own cache (0: none).  scale 0 means
+ * 1/sqrt(head_dim).  Strides count elements, must be multiples of 8, and are
+ * those of dense tensors where 0: q [R, L, n_heads, head_dim], prefix_k and
+ * prefix_v [P, n_kv_heads, head_dim], kv_k and kv_v [R, T, n_kv_heads, head_dim]
+ * (head_dim is dense; any order of the others will do).
+ * R <= 65535, R * L * n_heads <= 2^24. */
+typedef struct mtp_prefix_dims {
+  int R, L, n_heads, n_kv_heads, head_dim, P, T, causal;
+  float scale;
+  long long q_stride_r, q_stride_t, q_stride_h;
+  long long prefix_stride_t, prefix_stride_h;
+  long long kv_stride_r, kv_stride_t, kv_stride_h;
+} mtp_prefix_dims;
+
+/* Bytes of device workspace mtp_prefix_attention needs on the current device
+ * (0 if the sizes are invalid). */
+size_t mtp_prefix_attention_workspace_bytes(const mtp_prefix_dims* dims);
+
+/* Attention of a batch whose requests share a prefix ([M7.6] §0x09A: the module
+ * serves attention from its own K/V cache; here the rows of a common prompt are
+ * kept, and read, once for the batch).  For request r, new token i and head h
+ *   out = softmax(scale q [Kp; Kr]^T) [Vp; Vr]
+ * over all P prefix rows and the rows j of the request's own cache with
+ *   j < ctx_len[r] - (L - 1 - i)   if causal (the last L rows are the new
+ *                                  tokens' own: each sees itself and what precedes it),
+ *   j < ctx_len[r]                 otherwise.
+ * The cache rows from ctx_len[r] on are not used and may hold anything.  Keys
+ * are used as stored.  A token that sees no row gets zeros (and lse = -inf).
+ *   q, prefix_k, prefix_v, kv_k, kv_v: bf16, 16-byte aligned; ctx_len [R]
+ *   int32, nullable (T), clamped to [0, T]; out [R, L, n_heads, head_dim] bf16;
+ *   lse [R, L, n_heads] float, nullable: the natural logarithm of the softmax's
+ *   denominator with the maximum put back in.
+ *   ws: mtp_prefix_attention_workspace_bytes(dims) bytes, 16-byte aligned; calls
+ *   that may overlap need workspaces of their own.
+ * Scores, softmax statistics and outputs are fp32; the softmax weights enter
+ * the product with the values as bf16. */
+mtp_status mtp_prefix_attention(const mtp_prefix_dims* dims, const void* q, const void* prefix_k, const void* prefix_v,
+                                const void* kv_k, const void* kv_v, const int32_t* ctx_len, void* out, float* lse,
+                                void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* One FP8 block-scaled weight matrix W [n, K] ([M7.6] §0x03C: released
  * weights are FP8 with block scales; the runtime chooses the compute

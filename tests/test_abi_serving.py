@@ -50,3 +50,28 @@ def test_gemm_int4w_host_validation(lib):
     assert call(K=40) == 3 and call(x=ODD) == 3 and call(q=(1 << 20) + 8) == 3 and call(scale=(1 << 20) + 1) == 3
     assert call(out=ODD) == 3
     assert call(group=48) == 7 and call(group=256) == 7
+
+
+def test_prefix_attention_host_validation(lib):
+    from deepseek_sequential_mtp_gb300 import lib as binding
+
+    def call(q=FAKE, pk=FAKE, pv=FAKE, kk=FAKE, kv=FAKE, ctx=FAKE, out=FAKE, lse=FAKE, ws=FAKE, ws_bytes=1 << 40, **kw):
+        d = binding.PrefixDims(2, 1, 4, 2, 64, 20, 10, 1, 0.0)
+        for k, v in kw.items():
+            setattr(d, k, v)
+        return lib.mtp_prefix_attention(ctypes.byref(d), q, pk, pv, kk, kv, ctx, out, lse, ws, ws_bytes, None)
+
+    assert lib.mtp_prefix_attention(None, *[FAKE] * 9, 1 << 40, None) == 1
+    assert call(head_dim=96) == 7
+    for bad in (dict(R=0), dict(L=0), dict(n_heads=3), dict(n_kv_heads=0), dict(P=-1), dict(T=-1), dict(R=65536),
+                dict(R=1 << 10, L=1 << 10, n_heads=32)):
+        assert call(**bad) == 2
+        d = binding.PrefixDims(2, 1, 4, 2, 64, 20, 10, 1, 0.0)
+        for k, v in bad.items():
+            setattr(d, k, v)
+        assert lib.mtp_prefix_attention_workspace_bytes(ctypes.byref(d)) == 0
+    assert call(scale=-1.0) == 1 and call(scale=float("nan")) == 1
+    assert call(q=None) == 1 and call(pk=None) == 1 and call(kv=None) == 1 and call(out=None) == 1 and call(ws=None) == 1
+    assert call(q=ODD) == 3 and call(lse=ODD) == 3 and call(ctx=ODD) == 3 and call(q_stride_h=68) == 3
+    assert call(kv_stride_t=-8) == 2
+    assert call(ws_bytes=64) == 4
