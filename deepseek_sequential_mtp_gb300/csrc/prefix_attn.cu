@@ -11,28 +11,31 @@
 //
 // All rows that see the same keys form one matrix: for the prefix the R L G rows
 // (G = query heads per key head) of all requests, for a request's own cache its
-// L G rows.  Work is cut into items -- (key head, up to 256 rows) over the prefix,
-// (request, key head, up to 256 rows) over its cache -- and an item into blocks
-// of 128 keys.  The blocks of all items, weighted by their cost, are dealt to the
-// CTAs in equal contiguous ranges, whatever the lengths; a CTA's range within an
-// item (a segment) leaves one record of partial results per row, and a second
-// kernel joins a row's records.  Both kernels work the deal out from ctx_len.
+// L G rows.  A row tile is as many whole requests as fit into 128 rows (or, with
+// L G > 128, as many whole tokens of one request), so that one TMA box brings its
+// q.  Work is cut into items -- (key head, one or two row tiles) over the prefix,
+// (request, key head, one or two row tiles) over its cache -- and an item into
+// blocks of 128 keys.  The blocks of all items, weighted by their cost, are dealt
+// to the CTAs in equal contiguous ranges, whatever the lengths; a CTA's range
+// within an item (a segment) leaves one record of partial results per row, and a
+// second kernel joins a row's records.  Both kernels work the deal out from ctx_len.
 //
-// A segment runs as in the chain's attention: TMA brings K and V blocks, S = Q K^T
-// and O += P V run on tcgen05 with S, P and O in TMEM, a softmax thread owns a
-// row.  TMEM holds two tiles (S and P share columns), each with its own
-// warpgroup.  With more than 128 rows the two tiles are rows 0-127 and 128-255
-// and share every K/V block; with up to 128 rows both tiles are the same rows
-// and take the blocks alternately, so that one's softmax runs under the other's
-// products, each with a maximum, a sum and an output of its own (two records).
-//   softmax    warps 0-3 tile 0, warps 4-7 tile 1
+// A segment runs as in the chain's attention: TMA brings Q, K and V blocks, S =
+// Q K^T and O += P V run on tcgen05 with S, P and O in TMEM, a softmax thread owns
+// a row.  TMEM holds two tiles (S and P share columns), each with its own
+// warpgroup.  With two row tiles both share every K/V block.  With one, the TMEM
+// tiles take the blocks alternately, so that one's softmax runs under the other's
+// products, each with a maximum, a sum and an output of its own (two records);
+// the alternation runs on from segment to segment, so that short segments overlap
+// as well.
+//   softmax    warps 0-3 TMEM tile 0, warps 4-7 tile 1
 //   TMA warp   lane 0 walks the deal, publishes the segments in a ring and loads
-//              K, lane 1 loads V
-//   Q warp     gathers the rows' q with cp.async into the swizzled layout
+//              Q and K, lane 1 loads V
 //   MMA warp   one thread issues every product
-// Keys past a request's ctx_len may hold anything: their scores are replaced, and
-// their V rows are cleared in shared memory (0 times NaN is NaN).  Every wait is
-// bounded.
+// Keys past a request's ctx_len may hold anything: a last block is loaded in
+// groups of 32 rows, as many as it needs, scores past the end are replaced, and
+// V rows past the end are cleared in shared memory (0 times NaN is NaN).  Every
+// wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -51,8 +54,15 @@ constexpr int kRows = 128;   // rows per tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;   // keys per block
 constexpr float kStaleMaxLog2 = 8.0f;  // a running maximum is replaced only when exceeded by 2^8
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-// cost of a block with one row tile and with two, for the deal
-constexpr int kCostOne = 3, kCostTwo = 5;
+// costs for the deal: a block with one row tile, with two, and what a segment
+// of a request's own cache costs besides
+#ifndef PF_ONE
+#define PF_ONE 6
+#define PF_TWO 11
+#define PF_SEG 5
+#endif
+constexpr int kCostOne = PF_ONE, kCostTwo = PF_TWO, kCostItem = PF_SEG;
+constexpr int kMostCost = kCostTwo + kCostItem;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -68,44 +78,59 @@ __device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// sizes of the two kinds of items, and where their records are
+// Sizes of the two kinds of items (over the prefix, over a request's own cache),
+// and where their records are.
 struct Shape {
-  int R, L, H, Hkv, G, hd, P, T, causal;
-  int prefix_rows, prefix_tiles, prefix_blocks, prefix_cost;  // rows per key head; items per key head; ...
-  int own_rows, own_tiles, own_cost;
-  int prefix_rec, own_rec;      // record rows per segment
-  long long own_rec0;           // record row of the first own segment
+  int R, L, H, Hkv, G, P, T, causal;
+  int tokens;        // new tokens of a request per row tile (L, or as many as fit)
+  int groups;        // token groups per request: ceil(L / tokens)
+  int requests;      // requests per row tile of the prefix
+  int prefix_tiles, prefix_items, prefix_blocks, prefix_cost;  // row tiles and items per key head; blocks; cost of one
+  int own_items, own_cost;  // row tiles of an own item: `groups` per key head
+  int prefix_rec, own_rec;  // record rows per row tile
+  long long own_rec0;       // record row of the first own segment
   int grid;
   const int32_t* ctx_len;
 
-  __host__ __device__ int blocks_of(int len) const { return (len + kKeys - 1) / kKeys; }
+  __host__ __device__ static int blocks_of(int len) { return (len + kKeys - 1) / kKeys; }
   __device__ __forceinline__ int ctx(int r) const { return ctx_len ? min(max(ctx_len[r], 0), T) : T; }
   __host__ __device__ long long prefix_total() const {
-    return static_cast<long long>(Hkv) * prefix_tiles * prefix_blocks * prefix_cost;
+    return static_cast<long long>(Hkv) * prefix_items * prefix_blocks * prefix_cost;
   }
-  // cost of one block of a request's cache over all its heads and row tiles
-  __host__ __device__ long long own_step() const { return static_cast<long long>(Hkv) * own_tiles * own_cost; }
+  // cost of an item over `blocks` blocks of an own cache, and of all such items of the request
+  __host__ __device__ long long own_item(int blocks) const {
+    return blocks > 0 ? static_cast<long long>(blocks) * own_cost + kCostItem : 0;
+  }
+  __host__ __device__ long long own_total(int blocks) const { return own_item(blocks) * Hkv * own_items; }
 };
 
 // The deal: CTA k takes the blocks that start in [k total / n, (k + 1) total / n),
-// n so small that every CTA gets a block.
+// n so small that every CTA gets a block.  The first block of an own item starts
+// kCostItem before its cost, the others follow one another.
 struct Deal {
   long long total;
   int n;
-  __device__ __forceinline__ Deal(const Shape& s, long long own_blocks) {
-    total = s.prefix_total() + own_blocks * s.own_step();
-    const long long most = total / kCostTwo;
+  __device__ __forceinline__ Deal(const Shape& s, long long own) {
+    total = s.prefix_total() + own;
+    const long long most = total / kMostCost;
     n = static_cast<int>(most < 1 ? 1 : most < s.grid ? most : s.grid);
   }
   __device__ __forceinline__ long long start(int k) const { return k * total / n; }
   // the CTA whose range the position is in
   __device__ __forceinline__ int owner(long long pos) const { return static_cast<int>(((pos + 1) * n + total - 1) / total - 1); }
+  // blocks of an item (at `at`, its first block `extra` longer) that start before pos
+  static __device__ __forceinline__ int before(long long pos, long long at, int extra, int cost, int blocks) {
+    if (pos <= at) return 0;
+    const long long later = pos - at - extra;  // block j >= 1 starts at extra + j cost
+    const long long n = later > cost ? 1 + (later + cost - 1) / cost - 1 : 1;
+    return static_cast<int>(n < blocks ? n : blocks);
+  }
 };
 
 // a segment: blocks [b0, b0 + n) of an item
 struct Segment {
   int kind;  // bit 0: own cache (else prefix), bit 1: two row tiles; -1 ends
-  int head, tile, r;
+  int head, item, r;
   int b0, n, keys;  // keys: of the item
   int rec;          // index of its records among the kind's
 };
@@ -114,8 +139,8 @@ static_assert(sizeof(Segment) == 32, "two 16-byte words in the ring");
 template <int HD>
 struct Cfg {
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kTmaWarp = 8, kQWarp = 9, kMmaWarp = 10;
-  static constexpr int kThreads = 32 * 11;
+  static constexpr int kTmaWarp = 8, kMmaWarp = 9;
+  static constexpr int kThreads = 32 * 10;
   static constexpr int kChunks = HD / 64;
   static constexpr int kPiece = 128 * 128;       // one [128 rows x 128 B] swizzled piece
   static constexpr int kTileBytes = kRows * HD * 2;  // a Q, K or V tile
@@ -125,8 +150,8 @@ struct Cfg {
   static constexpr int kOffK = kQTiles * kTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-  static constexpr int kRing = 4;
-  static constexpr int kReaders = 3 + kSoftmaxWarps;  // V lane, Q warp, MMA thread, softmax warps
+  static constexpr int kRing = 8;
+  static constexpr int kReaders = 2 + kSoftmaxWarps;  // V lane, MMA thread, softmax warps
   // q, k, v full/empty; per tile s_full, p_full, pv_done, o_free; drain; segment ring full/empty
   static constexpr int kNumBars = 2 * (kQTiles + kKStages + kVStages) + 8 + 1 + 2 * kRing;
   static constexpr int kOffRing = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
@@ -134,12 +159,16 @@ struct Cfg {
   static constexpr uint32_t kColO = 256;
 };
 
+// tensor maps: q in boxes of a prefix tile's and of an own tile's rows; keys and
+// values in boxes of 128 (64) rows, the own caches' also of 32
+struct Maps {
+  CUtensorMap q_prefix, q_own, pk, pv, kk, kv, kk32, kv32;
+};
+
 template <int HD>
 __global__ void __launch_bounds__(Cfg<HD>::kThreads, 1)
-prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant__ CUtensorMap pv,
-                   const __grid_constant__ CUtensorMap kk, const __grid_constant__ CUtensorMap kv, const Shape sh,
-                   const __nv_bfloat16* __restrict__ q, long long q_r, long long q_l, long long q_h, float scale_log2,
-                   float2* __restrict__ rec_ml, float* __restrict__ rec_o) {
+prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_log2, float2* __restrict__ rec_ml,
+                   float* __restrict__ rec_o) {
   using C = Cfg<HD>;
   pdl_trigger();  // the joining kernel may start its setup
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -173,7 +202,7 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kQTiles; ++i) {
-      mbar_init(q_full(i), 32);
+      mbar_init(q_full(i), 1);
       mbar_init(q_empty(i), 1);
     }
     for (int i = 0; i < C::kKStages; ++i) {
@@ -223,64 +252,84 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
     if (lane == 0) mbar_arrive1(seg_empty(i));
     return true;
   };
-  auto first_row = [&](const Segment& s) { return s.tile * 2 * kRows; };
 
   if (warp == C::kTmaWarp) {
     // ---------------- TMA producers: lane 0 the deal and K, lane 1 V ----------------
-    // blocks of all own caches, then the request that this CTA's range starts in
+    // cost of all own caches, then the request that this CTA's range starts in
     long long own = 0;
-    for (int r = lane; r < sh.R; r += 32) own += sh.blocks_of(sh.ctx(r));
+    for (int r = lane; r < sh.R; r += 32) own += sh.own_total(sh.blocks_of(sh.ctx(r)));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
     const Deal deal(sh, own);
     const int cta = static_cast<int>(blockIdx.x);
-    const long long prefix_total = sh.prefix_total(), step = sh.own_step();
+    const long long prefix_total = sh.prefix_total();
     long long pos = cta < deal.n ? deal.start(cta) : 0;
     const long long end = cta < deal.n ? deal.start(cta + 1) : 0;
     int r0 = 0;
-    long long before = 0;  // own blocks of the requests before r0
+    long long at0 = prefix_total;  // where request r0 starts
     if (end > pos && end > prefix_total) {
-      const long long want = pos > prefix_total ? (pos - prefix_total) / step : 0;  // a block, over all requests
+      const long long want = max(pos, prefix_total);
       for (int base = 0; base < sh.R; base += 32) {
-        const int nb = base + lane < sh.R ? sh.blocks_of(sh.ctx(base + lane)) : 0;
-        int incl = nb;
+        const long long c = base + lane < sh.R ? sh.own_total(sh.blocks_of(sh.ctx(base + lane))) : 0;
+        long long incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int up = __shfl_up_sync(0xffffffffu, incl, o);
+          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += up;
         }
-        const unsigned over = __ballot_sync(0xffffffffu, before + incl > want);
+        const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > want);
         if (over) {
           const int src = __ffs(over) - 1;
           r0 = base + src;
-          before += __shfl_sync(0xffffffffu, incl - nb, src);
+          at0 += __shfl_sync(0xffffffffu, incl - c, src);
           break;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        at0 += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
     if (lane < 2) {
       const bool kside = lane == 0;
       const uint32_t stages = kside ? C::kKStages : C::kVStages;
-      uint32_t g = 0;
+      uint32_t g = 0, tile = 0;
       bool ok = true;
-      auto load = [&](const Segment& s) {  // the segment's blocks
+      auto load = [&](const Segment& s) {  // the segment's row tiles and blocks
+        const bool own_kind = s.kind & 1;
+        if (kside) {
+          for (int x = 0; x < (s.kind & 2 ? 2 : 1); ++x, ++tile) {
+            const uint32_t use = tile / C::kQTiles;
+            if (use > 0 && !wait(q_empty(tile), (use - 1) & 1)) { ok = false; return; }
+            const int t = 2 * s.item + x;  // row tile
+            const CUtensorMap* m = own_kind ? &maps.q_own : &maps.q_prefix;
+            const int r = own_kind ? s.r : t / sh.groups * sh.requests, tok = t % sh.groups * sh.tokens;
+            mbar_expect_tx(q_full(tile), (own_kind ? sh.own_rec : sh.prefix_rec) * HD * 2);
+            for (int c = 0; c < C::kChunks; ++c)
+              tma_tile_4d(sQ + (tile % C::kQTiles) * C::kTileBytes + c * C::kPiece, m, 64 * c, s.head * sh.G, tok, r,
+                          q_full(tile));
+          }
+        }
         for (int j = 0; j < s.n; ++j, ++g) {
           const uint32_t use = g / stages;
           if (use > 0 && !wait(kside ? k_empty(g) : v_empty(g), (use - 1) & 1)) { ok = false; return; }
           const int key = (s.b0 + j) * kKeys;
-          if (kside) {
-            const CUtensorMap* m = s.kind & 1 ? &kk : &pk;
-            mbar_expect_tx(k_full(g), C::kTileBytes);
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_tile_4d(sK + (g % C::kKStages) * C::kTileBytes + c * C::kPiece, m, 64 * c, s.head, key, s.r, k_full(g));
+          const uint32_t bar = kside ? k_full(g) : v_full(g);
+          const uint32_t dst = kside ? sK + (g % C::kKStages) * C::kTileBytes : sV + (g % C::kVStages) * C::kTileBytes;
+          if (own_kind && s.keys - key <= kKeys - 32) {  // the last block of a cache, in groups of 32 rows
+            const int n32 = (s.keys - key + 31) / 32;
+            mbar_expect_tx(bar, n32 * 32 * HD * 2);
+            for (int i = 0; i < n32; ++i)
+              for (int c = 0; c < C::kChunks; ++c)
+                tma_tile_4d(kside ? dst + c * C::kPiece + i * 4096 : dst + ((i >> 1) * C::kChunks + c) * 8192 + (i & 1) * 4096,
+                            kside ? &maps.kk32 : &maps.kv32, 64 * c, s.head, key + 32 * i, s.r, bar);
+          } else if (kside) {
+            const CUtensorMap* m = own_kind ? &maps.kk : &maps.pk;
+            mbar_expect_tx(bar, C::kTileBytes);
+            for (int c = 0; c < C::kChunks; ++c) tma_tile_4d(dst + c * C::kPiece, m, 64 * c, s.head, key, s.r, bar);
           } else {
-            const CUtensorMap* m = s.kind & 1 ? &kv : &pv;
-            mbar_expect_tx(v_full(g), C::kTileBytes);
+            const CUtensorMap* m = own_kind ? &maps.kv : &maps.pv;
+            mbar_expect_tx(bar, C::kTileBytes);
             for (int half = 0; half < 2; ++half)
               for (int c = 0; c < C::kChunks; ++c)
-                tma_tile_4d(sV + (g % C::kVStages) * C::kTileBytes + (half * C::kChunks + c) * 8192, m, 64 * c, s.head,
-                            key + 64 * half, s.r, v_full(g));
+                tma_tile_4d(dst + (half * C::kChunks + c) * 8192, m, 64 * c, s.head, key + 64 * half, s.r, bar);
           }
         }
       };
@@ -288,50 +337,47 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
         uint32_t i = 0;
         auto publish = [&](const Segment& s) {
           if (i >= static_cast<uint32_t>(C::kRing) && !wait(seg_empty(i), (i / C::kRing - 1) & 1)) { ok = false; return; }
-          ring[2 * (i % C::kRing)] = make_int4(s.kind, s.head, s.tile, s.r);
+          ring[2 * (i % C::kRing)] = make_int4(s.kind, s.head, s.item, s.r);
           ring[2 * (i % C::kRing) + 1] = make_int4(s.b0, s.n, s.keys, s.rec);
           mbar_arrive1(seg_full(i));
           ++i;
           if (s.kind >= 0) load(s);
         };
-        // blocks of the item that starts at `at` which start in [pos, end)
-        auto cut = [&](long long at, int blocks, int cost, Segment& s) {
-          const long long lo = pos > at ? (pos - at + cost - 1) / cost : 0;
-          const long long hi = end > at ? (end - at + cost - 1) / cost : 0;
-          s.b0 = static_cast<int>(min(lo, static_cast<long long>(blocks)));
-          s.n = static_cast<int>(min(hi, static_cast<long long>(blocks))) - s.b0;
+        // the blocks of the item at `at` that start in [pos, end)
+        auto cut = [&](long long at, int extra, int cost, int blocks, Segment& s) {
+          s.b0 = Deal::before(pos, at, extra, cost, blocks);
+          s.n = Deal::before(end, at, extra, cost, blocks) - s.b0;
           return s.n > 0;
         };
         if (pos < prefix_total) {
           const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
-          for (int item = static_cast<int>(pos / cost); ok && item < sh.Hkv * sh.prefix_tiles && item * cost < end; ++item) {
+          for (int k = static_cast<int>(pos / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < end; ++k) {
             Segment s;
-            s.head = item / sh.prefix_tiles;
-            s.tile = item - s.head * sh.prefix_tiles;
-            s.kind = sh.prefix_rows - first_row(s) > kRows ? 2 : 0;
+            s.head = k / sh.prefix_items;
+            s.item = k - s.head * sh.prefix_items;
+            s.kind = 2 * s.item + 1 < sh.prefix_tiles ? 2 : 0;
             s.r = 0;
             s.keys = sh.P;
-            s.rec = item + cta;
-            if (cut(item * cost, sh.prefix_blocks, sh.prefix_cost, s)) publish(s);
+            s.rec = k + cta;
+            if (cut(k * cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
           }
         }
-        const int per_r = sh.Hkv * sh.own_tiles;
-        for (int r = r0; ok && end > prefix_total && r < sh.R; ++r) {
+        const int per_r = sh.Hkv * sh.own_items;
+        for (int r = r0; ok && end > prefix_total && r < sh.R && at0 < end; ++r) {
           const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
-          const long long at0 = prefix_total + before * step, cost = static_cast<long long>(nb) * sh.own_cost;
-          if (at0 >= end) break;
-          before += nb;
-          if (nb == 0) continue;
-          for (int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0; ok && h < per_r && at0 + h * cost < end; ++h) {
-            Segment s;
-            s.head = h / sh.own_tiles;
-            s.tile = h - s.head * sh.own_tiles;
-            s.kind = 1 | (sh.own_rows - first_row(s) > kRows ? 2 : 0);
-            s.r = r;
-            s.keys = keys;
-            s.rec = r * per_r + h + cta;
-            if (cut(at0 + h * cost, nb, sh.own_cost, s)) publish(s);
-          }
+          const long long cost = sh.own_item(nb);
+          if (nb > 0)
+            for (int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0; ok && h < per_r && at0 + h * cost < end; ++h) {
+              Segment s;
+              s.head = h / sh.own_items;
+              s.item = h - s.head * sh.own_items;
+              s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
+              s.r = r;
+              s.keys = keys;
+              s.rec = r * per_r + h + cta;
+              if (cut(at0 + h * cost, kCostItem, sh.own_cost, nb, s)) publish(s);
+            }
+          at0 += cost * per_r;
         }
         Segment last{};
         last.kind = -1;
@@ -343,34 +389,9 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
       // no copy may still be landing when the CTA leaves (matters only after an abort)
       for (uint32_t x = g > stages ? g - stages : 0; x < g; ++x)
         wait_drain(kside ? k_full(x) : v_full(x), (x / stages) & 1, kWaitLimitCycles);
-    }
-  } else if (warp == C::kQWarp) {
-    // ---------------- Q: rows gathered into the 128-byte swizzled layout ----------------
-    Segment s;
-    uint32_t tile = 0;
-    bool ok = true;
-    for (uint32_t i = 0; ok && read_segment_warp(i, s); ++i) {
-      const int n_tiles = s.kind & 2 ? 2 : 1, rows = s.kind & 1 ? sh.own_rows : sh.prefix_rows;
-      for (int x = 0; ok && x < n_tiles; ++x, ++tile) {
-        const uint32_t use = tile / C::kQTiles;
-        if (use > 0 && !__all_sync(0xffffffffu, wait(q_empty(tile), (use - 1) & 1))) { ok = false; break; }
-        const uint32_t dst = sQ + (tile % C::kQTiles) * C::kTileBytes;
-        // 16-byte pieces: HD / 8 lanes per row
-        constexpr int kPer = HD / 8, kStep = 32 / kPer;
-        const int piece = lane % kPer;
-        for (int row = lane / kPer; row < kRows; row += kStep) {
-          const int rho = first_row(s) + x * kRows + row;
-          const bool live = rho < rows;
-          const int token = live ? rho / sh.G : 0, hg = live ? rho - token * sh.G : 0;
-          const int rr = s.kind & 1 ? s.r : token / sh.L, ll = s.kind & 1 ? token : token - rr * sh.L;
-          const __nv_bfloat16* src = q + rr * q_r + ll * q_l + (s.head * sh.G + hg) * q_h + piece * 8;
-          const uint32_t at = dst + (piece >> 3) * C::kPiece + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(src), "r"(live ? 16 : 0) : "memory");
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive1(q_full(tile));
-      }
+      if (kside)
+        for (uint32_t x = tile > C::kQTiles ? tile - C::kQTiles : 0; x < tile; ++x)
+          wait_drain(q_full(x), (x / C::kQTiles) & 1, kWaitLimitCycles);
     }
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issuer ----------------
@@ -378,102 +399,107 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
       constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
       uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
+      uint32_t turn = 0;            // blocks with one row tile so far: the TMEM tile is its parity
       uint32_t ns[2] = {0u, 0u};    // S products issued per TMEM tile
-      uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose output has been read
+      uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose first P V has been issued
       bool ok = true, any = false;
+      // S_x = Q K^T of row tile `qt` and ring block gu; the P that shared its columns was read by a
+      // product issued before
+      auto issue_s = [&](int x, uint32_t qt, uint32_t gu) {
+        const uint32_t q_at = sQ + (qt % C::kQTiles) * C::kTileBytes;
+        const uint32_t k_at = sK + (gu % C::kKStages) * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k >> 2) * C::kPiece + (k & 3) * 32;
+          umma_bf16_ss(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
+        }
+        umma_commit(s_full(x));
+        ++ns[x];
+        any = true;
+      };
+      auto wait_q = [&](uint32_t qt) { return wait(q_full(qt), (qt / C::kQTiles) & 1); };
+      auto wait_k = [&](uint32_t gu) {
+        if (!wait(k_full(gu), (gu / C::kKStages) & 1)) return false;
+        tc_fence_after();
+        return true;
+      };
+      // O_x (+)= P_x V of ring block gu, P_x from tile x's last S
+      auto issue_pv = [&](int x, uint32_t gu, bool first) {
+        if (!wait(p_full(x), (ns[x] - 1) & 1)) return false;
+        if (first) {
+          if (no[x] > 0 && !wait(o_free(x), (no[x] - 1) & 1)) return false;
+          ++no[x];
+        }
+        tc_fence_after();
+        const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k) {
+          const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
+          umma_bf16_ts(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
+                       (!first || k > 0) ? 1u : 0u);
+        }
+        umma_commit(pv_done(x));
+        return true;
+      };
+      auto wait_v = [&](uint32_t gu) { return wait(v_full(gu), (gu / C::kVStages) & 1); };
+      // with one row tile: the product of the block whose S was issued last waits until the
+      // next block's S (of the other TMEM tile, of the next segment too) has been issued
+      bool pending = false, pending_first = false;
+      int pending_x = 0;
+      uint32_t pending_g = 0;
+      auto flush = [&]() {
+        if (!pending) return true;
+        pending = false;
+        if (!wait_v(pending_g) || !issue_pv(pending_x, pending_g, pending_first)) return false;
+        umma_commit(v_empty(pending_g));
+        return true;
+      };
       Segment s;
       for (uint32_t i = 0; ok && read_segment(i, s); ++i) {
-        const bool two = s.kind & 2;
         const int n = s.n;
-        bool first_pv[2] = {true, true};
-        for (int x = 0; ok && x < (two ? 2 : 1); ++x)
-          if (!wait(q_full(tile + x), ((tile + x) / C::kQTiles) & 1)) ok = false;
-        if (!ok) break;
-        tc_fence_after();
-        // S_x = Q K^T of ring block gu; the P that shared its columns was read by a product issued before
-        auto issue_s = [&](int x, uint32_t gu) {
-          const uint32_t q_at = sQ + ((tile + (two ? x : 0)) % C::kQTiles) * C::kTileBytes;
-          const uint32_t k_at = sK + (gu % C::kKStages) * C::kTileBytes;
-#pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t off = (k >> 2) * C::kPiece + (k & 3) * 32;
-            umma_bf16_ss(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
+        if (!(s.kind & 2)) {
+          if (!wait_q(tile)) { ok = false; break; }
+          for (int j = 0; j < n && ok; ++j, ++turn, ++g) {
+            const int x = turn & 1;
+            if (!wait_k(g)) { ok = false; break; }
+            issue_s(x, tile, g);
+            umma_commit(k_empty(g));
+            if (j + 1 == n) umma_commit(q_empty(tile));
+            if (!flush()) { ok = false; break; }
+            pending = true;
+            pending_x = x;
+            pending_g = g;
+            pending_first = j < 2;  // the segment's first block on this TMEM tile
           }
-          umma_commit(s_full(x));
-          ++ns[x];
-          any = true;
-        };
-        auto wait_k = [&](uint32_t gu) {
-          if (!wait(k_full(gu), (gu / C::kKStages) & 1)) return false;
-          tc_fence_after();
-          return true;
-        };
-        // O_x (+)= P_x V of ring block gu
-        auto issue_pv = [&](int x, uint32_t gu) {
-          if (!wait(p_full(x), (ns[x] - 1) & 1)) return false;
-          if (first_pv[x] && no[x] > 0 && !wait(o_free(x), (no[x] - 1) & 1)) return false;
-          tc_fence_after();
-          const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k) {
-            const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
-            umma_bf16_ts(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
-                         (!first_pv[x] || k > 0) ? 1u : 0u);
-          }
-          umma_commit(pv_done(x));
-          first_pv[x] = false;
-          return true;
-        };
-        auto release_q = [&]() {
-          umma_commit(q_empty(tile));
-          if (two) umma_commit(q_empty(tile + 1));
-        };
-        if (two) {
-          if (!wait_k(g)) { ok = false; break; }
-          issue_s(0, g);
-          issue_s(1, g);
+          ++tile;
+        } else {
+          if (!flush() || !wait_q(tile) || !wait_q(tile + 1) || !wait_k(g)) { ok = false; break; }
+          issue_s(0, tile, g);
+          issue_s(1, tile + 1, g);
           umma_commit(k_empty(g));
-          if (n == 1) release_q();
           for (int j = 0; j < n && ok; ++j) {
             const uint32_t gu = g + j;
-            if (!wait(v_full(gu), (gu / C::kVStages) & 1)) { ok = false; break; }
+            if (j + 1 == n) {
+              umma_commit(q_empty(tile));
+              umma_commit(q_empty(tile + 1));
+            }
+            if (!wait_v(gu)) { ok = false; break; }
             for (int x = 0; x < 2 && ok; ++x) {
-              if (!issue_pv(x, gu)) { ok = false; break; }
+              if (!issue_pv(x, gu, j == 0)) { ok = false; break; }
               if (j + 1 < n) {
                 if (x == 0 && !wait_k(gu + 1)) { ok = false; break; }
-                issue_s(x, gu + 1);
+                issue_s(x, tile + x, gu + 1);
               }
             }
             if (!ok) break;
             umma_commit(v_empty(gu));
             if (j + 1 < n) umma_commit(k_empty(gu + 1));
-            if (j + 2 == n) release_q();
           }
-        } else {
-          for (int j = 0; j < min(n, 2) && ok; ++j) {
-            if (!wait_k(g + j)) { ok = false; break; }
-            issue_s(j, g + j);
-            umma_commit(k_empty(g + j));
-          }
-          if (!ok) break;
-          if (n <= 2) release_q();
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t gu = g + j;
-            if (!wait(v_full(gu), (gu / C::kVStages) & 1) || !issue_pv(j & 1, gu)) { ok = false; break; }
-            umma_commit(v_empty(gu));
-            if (j + 2 < n) {
-              if (!wait_k(gu + 2)) { ok = false; break; }
-              issue_s(j & 1, gu + 2);
-              umma_commit(k_empty(gu + 2));
-              if (j + 3 == n) release_q();
-            }
-          }
+          g += n;
+          tile += 2;
         }
-        g += n;
-        tile += two ? 2 : 1;
-        ++no[0];
-        if (two || n > 1) ++no[1];
       }
+      if (ok) flush();
       // every issued MMA has completed before TMEM is freed
       if (any) {
         umma_commit(drain_bar);
@@ -487,25 +513,31 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t colS = 128u * x, colO = C::kColO + HD * x;
     auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-    uint32_t n = 0;  // S products of this tile consumed
-    uint32_t g = 0;  // key blocks of the CTA's earlier segments
+    uint32_t n = 0;     // S products of this tile consumed
+    uint32_t g = 0;     // key blocks of the CTA's earlier segments
+    uint32_t turn = 0;  // ... of them with one row tile
     Segment s;
     for (uint32_t i = 0; read_segment_warp(i, s); ++i) {
       const bool two = s.kind & 2, own = s.kind & 1;
-      const int rows = own ? sh.own_rows : sh.prefix_rows;
-      const int rho = first_row(s) + (two ? x * kRows : 0) + row;
-      const bool live = rho < rows;
-      const bool live_warp = first_row(s) + (two ? x * kRows : 0) + (warp & 3) * 32 < rows;
+      // this thread's row of the row tile: request, token
+      const int t = 2 * s.item + (two ? x : 0), per = sh.tokens * sh.G;
+      const int in = row / per;
+      const int token = t % sh.groups * sh.tokens + (row - in * per) / sh.G;
+      const int request = own ? s.r : t / sh.groups * sh.requests + in;
+      const bool live = in < (own ? 1 : sh.requests) && request < sh.R && token < sh.L;
+      const bool live_warp = __any_sync(0xffffffffu, live);
       // keys that the row sees
       int see = s.keys;
-      if (own && sh.causal) see = max(0, s.keys - sh.L + 1 + rho / sh.G);
-      const int mine = two ? s.n : (s.n + 1 - x) >> 1;  // blocks of this tile
+      if (own && sh.causal) see = max(0, s.keys - sh.L + 1 + token);
+      // this tile's blocks of the segment: first, step, number
+      const int j0 = two ? 0 : (turn ^ x) & 1, step = two ? 1 : 2;
+      const int mine = two ? s.n : (s.n - j0 + 1) >> 1;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       for (int j = 0; j < mine; ++j, ++n) {
         if (!wwait(s_full(x), n & 1)) { ok = false; break; }
         tc_fence_after();
-        const int jb = two ? j : 2 * j + x;
+        const int jb = j0 + j * step;
         const int key0 = (s.b0 + jb) * kKeys;
         if (own && s.keys - key0 < kKeys && (!two || x == 0)) {  // V rows past the end of the request's cache
           const uint32_t gu = g + jb;
@@ -579,9 +611,10 @@ prefix_attn_kernel(const __grid_constant__ CUtensorMap pk, const __grid_constant
       }
       if (!ok) break;
       g += s.n;
+      if (!two) turn += s.n;
       // the segment's record of this row (of this tile's half of them with one row tile)
       const int rec_rows = own ? sh.own_rec : sh.prefix_rec;
-      const long long at = (own ? sh.own_rec0 : 0) + static_cast<long long>(s.rec) * rec_rows + x * (rec_rows / 2) + row;
+      const long long at = (own ? sh.own_rec0 : 0) + (2ll * s.rec + x) * rec_rows + row;
       if (mine > 0) {
         if (!wwait(pv_done(x), (n - 1) & 1)) break;  // the segment's last P V
         tc_fence_after();
@@ -615,18 +648,21 @@ template <int HD>
 __global__ void __launch_bounds__(256)
 prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const float* __restrict__ rec_o,
                    __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
-  __shared__ int s_sum[8], s_before[8];
+  __shared__ long long s_sum[8], s_before[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y;
-  // own blocks of all requests, and of those before r
-  int sum = 0, before = 0;
+  // cost of all requests' own caches, and of those before r
+  long long sum = 0, before = 0;
   for (int i = threadIdx.x; i < sh.R; i += 256) {
-    const int nb = sh.blocks_of(sh.ctx(i));
-    sum += nb;
-    if (i < r) before += nb;
+    const long long c = sh.own_total(sh.blocks_of(sh.ctx(i)));
+    sum += c;
+    if (i < r) before += c;
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  before = __reduce_add_sync(0xffffffffu, before);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
   if (lane == 0) {
     s_sum[warp] = sum;
     s_before[warp] = before;
@@ -648,29 +684,28 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
     long long at;
     int n, rows, halves;
   } run[2];
+  const int group = i / sh.tokens, in = (i - group * sh.tokens) * sh.G + hg;  // row of a tile that starts at the request
   {
-    const int rho = (r * sh.L + i) * sh.G + hg, tile = rho / (2 * kRows), in = rho - tile * 2 * kRows;
-    const bool two = sh.prefix_rows - tile * 2 * kRows > kRows;
-    const int k = head * sh.prefix_tiles + tile;
+    const int tile = r / sh.requests * sh.groups + group, row = r % sh.requests * sh.tokens * sh.G + in;
+    const bool two = (tile | 1) < sh.prefix_tiles;
+    const int k = head * sh.prefix_items + tile / 2;
     const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost, at = k * cost;
-    run[0] = Run{0, 0, sh.prefix_rec, two ? 1 : 2};
+    run[0] = Run{0, 0, 2 * sh.prefix_rec, two ? 1 : 2};
     if (cost > 0) {
       const int a = deal.owner(at), b = deal.owner(at + cost - sh.prefix_cost);
       run[0].n = b - a + 1;
-      run[0].at = static_cast<long long>(k + a) * sh.prefix_rec + in;
+      run[0].at = (2ll * (k + a) + (two ? tile & 1 : 0)) * sh.prefix_rec + row;
     }
   }
   {
-    const int rho = i * sh.G + hg, tile = rho / (2 * kRows), in = rho - tile * 2 * kRows;
-    const bool two = sh.own_rows - tile * 2 * kRows > kRows;
-    const int nb = sh.blocks_of(sh.ctx(r)), k = head * sh.own_tiles + tile;
-    const long long cost = static_cast<long long>(nb) * sh.own_cost;
-    const long long at = sh.prefix_total() + prev * sh.own_step() + k * cost;
-    run[1] = Run{0, 0, sh.own_rec, two ? 1 : 2};
+    const bool two = (group | 1) < sh.groups;
+    const int nb = sh.blocks_of(sh.ctx(r)), k = head * sh.own_items + group / 2;
+    const long long cost = sh.own_item(nb), at = sh.prefix_total() + prev + k * cost;
+    run[1] = Run{0, 0, 2 * sh.own_rec, two ? 1 : 2};
     if (nb > 0) {
-      const int a = deal.owner(at), b = deal.owner(at + cost - sh.own_cost);
+      const int a = deal.owner(at), b = deal.owner(nb > 1 ? at + cost - sh.own_cost : at);
       run[1].n = b - a + 1;
-      run[1].at = sh.own_rec0 + static_cast<long long>(r * sh.Hkv * sh.own_tiles + k + a) * sh.own_rec + in;
+      run[1].at = sh.own_rec0 + (2ll * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
     }
   }
   const int n0 = run[0].n * run[0].halves, parts = n0 + run[1].n * run[1].halves;
@@ -702,22 +737,26 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
       }
     }
     const int n = min(32, parts - p0);
-#pragma unroll 4
-    for (int e = 0; e < n; ++e) {
-      const float we = __shfl_sync(0xffffffffu, w, e);
-      const long long ae = __shfl_sync(0xffffffffu, at, e);
-      if (we != 0.f) {  // warp-uniform (NaN too); a part without a key has no output to read
-        const float* src = rec_o + ae * HD + lane * kD;
+    // eight parts' outputs in flight; a part without a key has left none
+    for (int e0 = 0; e0 < n; e0 += 8) {
+      float v[8][kD];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float* src = rec_o + __shfl_sync(0xffffffffu, at, min(e0 + e, n - 1)) * HD + lane * kD;
         if constexpr (kD == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          acc[0] = fmaf(we, v.x, acc[0]);
-          acc[1] = fmaf(we, v.y, acc[1]);
-          acc[2] = fmaf(we, v.z, acc[2]);
-          acc[3] = fmaf(we, v.w, acc[3]);
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[e][0] = f.x; v[e][1] = f.y; v[e][2] = f.z; v[e][3] = f.w;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(src);
-          acc[0] = fmaf(we, v.x, acc[0]);
-          acc[1] = fmaf(we, v.y, acc[1]);
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[e][0] = f.x; v[e][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float we = __shfl_sync(0xffffffffu, w, min(e0 + e, 31));
+        if (e0 + e < n && we != 0.f) {
+#pragma unroll
+          for (int d = 0; d < kD; ++d) acc[d] = fmaf(we, v[e][d], acc[d]);
         }
       }
     }
@@ -745,40 +784,41 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
 
 inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-Shape make_shape(int R, int L, int H, int Hkv, int hd, int P, int T) {
+Shape make_shape(int R, int L, int H, int Hkv, int P, int T) {
   Shape s{};
   s.R = R;
   s.L = L;
   s.H = H;
   s.Hkv = Hkv;
   s.G = H / Hkv;
-  s.hd = hd;
   s.P = P;
   s.T = T;
-  s.prefix_rows = R * L * s.G;
-  s.own_rows = L * s.G;
-  s.prefix_tiles = (s.prefix_rows + 2 * kRows - 1) / (2 * kRows);
-  s.own_tiles = (s.own_rows + 2 * kRows - 1) / (2 * kRows);
-  s.prefix_blocks = (P + kKeys - 1) / kKeys;
-  s.prefix_cost = s.prefix_rows > kRows ? kCostTwo : kCostOne;
-  s.own_cost = s.own_rows > kRows ? kCostTwo : kCostOne;
-  s.prefix_rec = s.prefix_rows > kRows ? 2 * kRows : 2 * s.prefix_rows;
-  s.own_rec = s.own_rows > kRows ? 2 * kRows : 2 * s.own_rows;
+  s.tokens = std::min(L, kRows / s.G);
+  s.groups = (L + s.tokens - 1) / s.tokens;
+  s.requests = s.groups > 1 ? 1 : std::min(R, kRows / (L * s.G));
+  s.prefix_tiles = (R + s.requests - 1) / s.requests * s.groups;
+  s.prefix_items = (s.prefix_tiles + 1) / 2;
+  s.prefix_blocks = Shape::blocks_of(P);
+  s.prefix_cost = s.prefix_tiles > 1 ? kCostTwo : kCostOne;
+  s.own_items = (s.groups + 1) / 2;
+  s.own_cost = s.groups > 1 ? kCostTwo : kCostOne;
+  s.own_rec = s.tokens * s.G;
+  s.prefix_rec = s.requests * s.own_rec;
   s.grid = sm_count_current();
-  s.own_rec0 = P > 0 ? (static_cast<long long>(Hkv) * s.prefix_tiles + s.grid) * s.prefix_rec : 0;
+  s.own_rec0 = P > 0 ? 2 * (static_cast<long long>(Hkv) * s.prefix_items + s.grid) * s.prefix_rec : 0;
   return s;
 }
 long long record_rows(const Shape& s) {
-  return s.own_rec0 + (s.T > 0 ? (static_cast<long long>(s.R) * s.Hkv * s.own_tiles + s.grid) * s.own_rec : 0);
+  return s.own_rec0 + (s.T > 0 ? 2 * (static_cast<long long>(s.R) * s.Hkv * s.own_items + s.grid) * s.own_rec : 0);
 }
 
-// keys or values as (dimension, head, token, request); boxes of 64 dimensions x `box` tokens of one head
-bool kv_map(CUtensorMap* m, const void* p, int hd, int heads, int tokens, int requests, long long s_h, long long s_t,
-            long long s_r, int box) {
+// rows as (dimension, head, token, request); boxes of 64 dimensions of heads x tokens x requests
+bool row_map(CUtensorMap* m, const void* p, int hd, int heads, int tokens, int requests, long long s_h, long long s_t,
+             long long s_r, int box_h, int box_t, int box_r) {
   const uint64_t dims[4] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(heads), static_cast<uint64_t>(tokens),
                             static_cast<uint64_t>(requests)};
   const uint64_t strides[3] = {static_cast<uint64_t>(s_h) * 2, static_cast<uint64_t>(s_t) * 2, static_cast<uint64_t>(s_r) * 2};
-  const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
+  const uint32_t boxes[4] = {64, static_cast<uint32_t>(box_h), static_cast<uint32_t>(box_t), static_cast<uint32_t>(box_r)};
   return tensor_map_bf16_4d(m, p, dims, strides, boxes);
 }
 
@@ -787,17 +827,21 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   using C = Cfg<HD>;
   static PerDevice attr;
   if (!smem_limit(attr, prefix_attn_kernel<HD>, C::kSmemBytes)) return MTP_ERR_CUDA;
-  CUtensorMap pk{}, pv{}, kk{}, kv{};
-  if (p.P > 0 && (!kv_map(&pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, kKeys) ||
-                  !kv_map(&pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 64)))
+  Maps m{};
+  if (!row_map(&m.q_prefix, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, s.requests) ||
+      !row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1))
     return MTP_ERR_CUDA;
-  if (p.T > 0 && (!kv_map(&kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, kKeys) ||
-                  !kv_map(&kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 64)))
+  if (p.P > 0 && (!row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, kKeys, 1) ||
+                  !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
+    return MTP_ERR_CUDA;
+  if (p.T > 0 && (!row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, kKeys, 1) ||
+                  !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1) ||
+                  !row_map(&m.kk32, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 32, 1) ||
+                  !row_map(&m.kv32, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 32, 1)))
     return MTP_ERR_CUDA;
   const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
   if (p.P > 0 || p.T > 0) {
-    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(pk, pv, kk, kv, s, p.q, p.q_r, p.q_l, p.q_h,
-                                                                      scale * kLog2e, ml, ro);
+    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(m, s, scale * kLog2e, ml, ro);
     note_launch();
     MTP_LAUNCH_CHECK();
   }
@@ -812,7 +856,7 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
 }
 
 bool sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T) {
-  return R >= 1 && R <= 65535 && L >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && (hd == 64 || hd == 128) && P >= 0 && T >= 0 &&
+  return R >= 1 && R <= 65535 && L >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= kRows && (hd == 64 || hd == 128) && P >= 0 && T >= 0 &&
          static_cast<long long>(R) * L * H <= (1 << 24) && static_cast<long long>(P) + T <= 0x7FFFFF00ll;
 }
 
@@ -820,14 +864,14 @@ bool sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T) {
 
 size_t prefix_attn_workspace_bytes(int R, int L, int H, int Hkv, int hd, int P, int T) {
   if (!sizes_ok(R, L, H, Hkv, hd, P, T)) return 0;
-  const long long rows = record_rows(make_shape(R, L, H, Hkv, hd, P, T));
+  const long long rows = record_rows(make_shape(R, L, H, Hkv, P, T));
   return up256(rows * sizeof(float2)) + up256(static_cast<size_t>(rows) * hd * 4) + 256;
 }
 
 mtp_status prefix_attn_launch(const PrefixAttn& p, void* ws, size_t ws_bytes, cudaStream_t st) {
   if (!sizes_ok(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_SHAPE;
   if (ws_bytes < prefix_attn_workspace_bytes(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_WORKSPACE;
-  Shape s = make_shape(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T);
+  Shape s = make_shape(p.R, p.L, p.H, p.Hkv, p.P, p.T);
   s.causal = p.causal;
   s.ctx_len = p.ctx_len;
   float2* ml = static_cast<float2*>(ws);

@@ -418,7 +418,7 @@ mtp_status mtp_draft_round(const mtp_dims* dims, const mtp_weights* w, const voi
  * those of dense tensors where 0: q [R, L, n_heads, head_dim], prefix_k and
  * prefix_v [P, n_kv_heads, head_dim], kv_k and kv_v [R, T, n_kv_heads, head_dim]
  * (head_dim is dense; any order of the others will do).
- * R <= 65535, R * L * n_heads <= 2^24. */
+ * R <= 65535, n_heads / n_kv_heads <= 128, R * L * n_heads <= 2^24. */
 typedef struct mtp_prefix_dims {
   int R, L, n_heads, n_kv_heads, head_dim, P, T, causal;
   float scale;
