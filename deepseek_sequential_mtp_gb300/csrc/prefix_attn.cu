@@ -29,8 +29,9 @@
 // the alternation runs on from segment to segment, so that short segments overlap
 // as well.
 //   softmax    warps 0-3 TMEM tile 0, warps 4-7 tile 1
-//   TMA warp   lane 0 walks the deal, publishes the segments in a ring and loads
-//              Q and K, lane 1 loads V
+//   K warp     walks the deal, publishes the segments in a ring and loads Q and K
+//   V warp     loads V (as a second lane of the K warp it stood still whenever the
+//              first was suspended in a wait: 4 us per short segment)
 //   MMA warp   one thread issues every product
 // Keys past a request's ctx_len may hold anything: a last block is loaded in
 // groups of 32 rows, as many as it needs, scores past the end are replaced, and
@@ -62,7 +63,6 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 #define PF_SEG 5
 #endif
 constexpr int kCostOne = PF_ONE, kCostTwo = PF_TWO, kCostItem = PF_SEG;
-constexpr int kMostCost = kCostTwo + kCostItem;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -104,15 +104,18 @@ struct Shape {
   __host__ __device__ long long own_total(int blocks) const { return own_item(blocks) * Hkv * own_items; }
 };
 
-// The deal: CTA k takes the blocks that start in [k total / n, (k + 1) total / n),
-// n so small that every CTA gets a block.  The first block of an own item starts
-// kCostItem before its cost, the others follow one another.
+// A deal of the prefix's blocks, and one of the own caches': CTA k takes the
+// blocks that start in [k total / n, (k + 1) total / n), n so small that every
+// CTA gets a block.  The first block of an own item costs kCostItem more.  Every
+// CTA works on the prefix first and then on own caches: in one deal over both,
+// the CTAs on the prefix kept the memory queues full, and those on short own
+// items waited 6 us for each of their loads.
 struct Deal {
   long long total;
   int n;
-  __device__ __forceinline__ Deal(const Shape& s, long long own) {
-    total = s.prefix_total() + own;
-    const long long most = total / kMostCost;
+  __device__ __forceinline__ Deal(const Shape& s, long long total_, int most_cost) {
+    total = total_;
+    const long long most = total / most_cost;
     n = static_cast<int>(most < 1 ? 1 : most < s.grid ? most : s.grid);
   }
   __device__ __forceinline__ long long start(int k) const { return k * total / n; }
@@ -139,19 +142,19 @@ static_assert(sizeof(Segment) == 32, "two 16-byte words in the ring");
 template <int HD>
 struct Cfg {
   static constexpr int kSoftmaxWarps = 8;
-  static constexpr int kTmaWarp = 8, kMmaWarp = 9;
-  static constexpr int kThreads = 32 * 10;
+  static constexpr int kKWarp = 8, kMmaWarp = 9, kVWarp = 10;
+  static constexpr int kThreads = 32 * 11;
   static constexpr int kChunks = HD / 64;
   static constexpr int kPiece = 128 * 128;       // one [128 rows x 128 B] swizzled piece
   static constexpr int kTileBytes = kRows * HD * 2;  // a Q, K or V tile
   static constexpr int kQTiles = HD == 64 ? 4 : 2;
-  static constexpr int kKStages = HD == 64 ? 4 : 3;
-  static constexpr int kVStages = HD == 64 ? 4 : 2;
+  static constexpr int kKStages = HD == 64 ? 4 : 2;
+  static constexpr int kVStages = HD == 64 ? 4 : 3;
   static constexpr int kOffK = kQTiles * kTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
   static constexpr int kRing = 8;
-  static constexpr int kReaders = 2 + kSoftmaxWarps;  // V lane, MMA thread, softmax warps
+  static constexpr int kReaders = 2 + kSoftmaxWarps;  // V thread, MMA thread, softmax warps
   // q, k, v full/empty; per tile s_full, p_full, pv_done, o_free; drain; segment ring full/empty
   static constexpr int kNumBars = 2 * (kQTiles + kKStages + kVStages) + 8 + 1 + 2 * kRing;
   static constexpr int kOffRing = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
@@ -253,22 +256,21 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
     return true;
   };
 
-  if (warp == C::kTmaWarp) {
-    // ---------------- TMA producers: lane 0 the deal and K, lane 1 V ----------------
-    // cost of all own caches, then the request that this CTA's range starts in
+  if (warp == C::kKWarp || warp == C::kVWarp) {
+    // ---------------- TMA producers: the deal, Q and K; V ----------------
+    const bool kside = warp == C::kKWarp;
+    // cost of all own caches, then the request that this CTA's range of them starts in
     long long own = 0;
-    for (int r = lane; r < sh.R; r += 32) own += sh.own_total(sh.blocks_of(sh.ctx(r)));
+    for (int r = lane; kside && r < sh.R; r += 32) own += sh.own_total(sh.blocks_of(sh.ctx(r)));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    const Deal deal(sh, own);
     const int cta = static_cast<int>(blockIdx.x);
     const long long prefix_total = sh.prefix_total();
-    long long pos = cta < deal.n ? deal.start(cta) : 0;
-    const long long end = cta < deal.n ? deal.start(cta + 1) : 0;
+    const Deal shared(sh, prefix_total, sh.prefix_cost), each(sh, own, sh.own_cost + kCostItem);
+    const long long pos = cta < each.n ? each.start(cta) : 0, end = cta < each.n ? each.start(cta + 1) : 0;
     int r0 = 0;
-    long long at0 = prefix_total;  // where request r0 starts
-    if (end > pos && end > prefix_total) {
-      const long long want = max(pos, prefix_total);
+    long long at0 = 0;  // where request r0 starts
+    if (kside && end > pos) {
       for (int base = 0; base < sh.R; base += 32) {
         const long long c = base + lane < sh.R ? sh.own_total(sh.blocks_of(sh.ctx(base + lane))) : 0;
         long long incl = c;
@@ -277,7 +279,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           const long long up = __shfl_up_sync(0xffffffffu, incl, o);
           if (lane >= o) incl += up;
         }
-        const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > want);
+        const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > pos);
         if (over) {
           const int src = __ffs(over) - 1;
           r0 = base + src;
@@ -287,8 +289,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         at0 += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    if (lane < 2) {
-      const bool kside = lane == 0;
+    if (lane == 0) {
       const uint32_t stages = kside ? C::kKStages : C::kVStages;
       uint32_t g = 0, tile = 0;
       bool ok = true;
@@ -299,8 +300,9 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
             const uint32_t use = tile / C::kQTiles;
             if (use > 0 && !wait(q_empty(tile), (use - 1) & 1)) { ok = false; return; }
             const int t = 2 * s.item + x;  // row tile
+            const int first = sh.groups > 1 ? t / sh.groups : own_kind ? 0 : t;  // request (of a prefix tile)
             const CUtensorMap* m = own_kind ? &maps.q_own : &maps.q_prefix;
-            const int r = own_kind ? s.r : t / sh.groups * sh.requests, tok = t % sh.groups * sh.tokens;
+            const int r = own_kind ? s.r : first * sh.requests, tok = (sh.groups > 1 ? t - first * sh.groups : 0) * sh.tokens;
             mbar_expect_tx(q_full(tile), (own_kind ? sh.own_rec : sh.prefix_rec) * HD * 2);
             for (int c = 0; c < C::kChunks; ++c)
               tma_tile_4d(sQ + (tile % C::kQTiles) * C::kTileBytes + c * C::kPiece, m, 64 * c, s.head * sh.G, tok, r,
@@ -343,15 +345,16 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           ++i;
           if (s.kind >= 0) load(s);
         };
-        // the blocks of the item at `at` that start in [pos, end)
-        auto cut = [&](long long at, int extra, int cost, int blocks, Segment& s) {
-          s.b0 = Deal::before(pos, at, extra, cost, blocks);
-          s.n = Deal::before(end, at, extra, cost, blocks) - s.b0;
+        // the blocks of the item at `at` that start in [from, to)
+        auto cut = [&](long long from, long long to, long long at, int extra, int cost, int blocks, Segment& s) {
+          s.b0 = Deal::before(from, at, extra, cost, blocks);
+          s.n = Deal::before(to, at, extra, cost, blocks) - s.b0;
           return s.n > 0;
         };
-        if (pos < prefix_total) {
+        if (cta < shared.n && prefix_total > 0) {
+          const long long from = shared.start(cta), to = shared.start(cta + 1);
           const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
-          for (int k = static_cast<int>(pos / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < end; ++k) {
+          for (int k = static_cast<int>(from / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < to; ++k) {
             Segment s;
             s.head = k / sh.prefix_items;
             s.item = k - s.head * sh.prefix_items;
@@ -359,11 +362,11 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
             s.r = 0;
             s.keys = sh.P;
             s.rec = k + cta;
-            if (cut(k * cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
+            if (cut(from, to, k * cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
           }
         }
         const int per_r = sh.Hkv * sh.own_items;
-        for (int r = r0; ok && end > prefix_total && r < sh.R && at0 < end; ++r) {
+        for (int r = r0; ok && r < sh.R && at0 < end; ++r) {
           const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
           const long long cost = sh.own_item(nb);
           if (nb > 0)
@@ -375,7 +378,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
               s.r = r;
               s.keys = keys;
               s.rec = r * per_r + h + cta;
-              if (cut(at0 + h * cost, kCostItem, sh.own_cost, nb, s)) publish(s);
+              if (cut(pos, end, at0 + h * cost, kCostItem, sh.own_cost, nb, s)) publish(s);
             }
           at0 += cost * per_r;
         }
@@ -516,14 +519,15 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
     uint32_t n = 0;     // S products of this tile consumed
     uint32_t g = 0;     // key blocks of the CTA's earlier segments
     uint32_t turn = 0;  // ... of them with one row tile
+    // this thread's row of a row tile: request and token from the tile's first
+    const int in = row / (sh.tokens * sh.G), at_token = (row - in * sh.tokens * sh.G) / sh.G;
     Segment s;
     for (uint32_t i = 0; read_segment_warp(i, s); ++i) {
       const bool two = s.kind & 2, own = s.kind & 1;
-      // this thread's row of the row tile: request, token
-      const int t = 2 * s.item + (two ? x : 0), per = sh.tokens * sh.G;
-      const int in = row / per;
-      const int token = t % sh.groups * sh.tokens + (row - in * per) / sh.G;
-      const int request = own ? s.r : t / sh.groups * sh.requests + in;
+      const int t = 2 * s.item + (two ? x : 0);
+      const int first = sh.groups > 1 ? t / sh.groups : own ? 0 : t;
+      const int token = (sh.groups > 1 ? t - first * sh.groups : 0) * sh.tokens + at_token;
+      const int request = own ? s.r : first * sh.requests + in;
       const bool live = in < (own ? 1 : sh.requests) && request < sh.R && token < sh.L;
       const bool live_warp = __any_sync(0xffffffffu, live);
       // keys that the row sees
@@ -678,7 +682,7 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
   const int item = blockIdx.x * 8 + warp;
   if (item >= sh.L * sh.H) return;
   const int i = item / sh.H, h = item - i * sh.H, head = h / sh.G, hg = h - head * sh.G;
-  const Deal deal(sh, all);
+  const Deal shared(sh, sh.prefix_total(), sh.prefix_cost), each(sh, all, sh.own_cost + kCostItem);
   // record rows: `n` segments from record row `at` on, `rows` apart, each with `halves` parts rows / 2 apart
   struct Run {
     long long at;
@@ -692,7 +696,7 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
     const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost, at = k * cost;
     run[0] = Run{0, 0, 2 * sh.prefix_rec, two ? 1 : 2};
     if (cost > 0) {
-      const int a = deal.owner(at), b = deal.owner(at + cost - sh.prefix_cost);
+      const int a = shared.owner(at), b = shared.owner(at + cost - sh.prefix_cost);
       run[0].n = b - a + 1;
       run[0].at = (2ll * (k + a) + (two ? tile & 1 : 0)) * sh.prefix_rec + row;
     }
@@ -700,10 +704,10 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
   {
     const bool two = (group | 1) < sh.groups;
     const int nb = sh.blocks_of(sh.ctx(r)), k = head * sh.own_items + group / 2;
-    const long long cost = sh.own_item(nb), at = sh.prefix_total() + prev + k * cost;
+    const long long cost = sh.own_item(nb), at = prev + k * cost;
     run[1] = Run{0, 0, 2 * sh.own_rec, two ? 1 : 2};
     if (nb > 0) {
-      const int a = deal.owner(at), b = deal.owner(nb > 1 ? at + cost - sh.own_cost : at);
+      const int a = each.owner(at), b = each.owner(nb > 1 ? at + cost - sh.own_cost : at);
       run[1].n = b - a + 1;
       run[1].at = sh.own_rec0 + (2ll * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
     }
