@@ -33,10 +33,10 @@
 //   V warp     loads V (as a second lane of the K warp it stood still whenever the
 //              first was suspended in a wait: 4 us per short segment)
 //   MMA warp   one thread issues every product
-// Keys past a request's ctx_len may hold anything: a last block is loaded in
-// groups of 32 rows, as many as it needs, scores past the end are replaced, and
-// V rows past the end are cleared in shared memory (0 times NaN is NaN).  Every
-// wait is bounded.
+// A last block is loaded as 64 rows where it has no more, and its products run
+// over as many groups of 16 keys as it has.  Keys past a request's ctx_len may
+// hold anything: their scores are replaced, and their V rows are cleared in
+// shared memory (0 times NaN is NaN).  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -162,10 +162,10 @@ struct Cfg {
   static constexpr uint32_t kColO = 256;
 };
 
-// tensor maps: q in boxes of a prefix tile's and of an own tile's rows; keys and
-// values in boxes of 128 (64) rows, the own caches' also of 32
+// tensor maps: q in boxes of a prefix tile's and of an own tile's rows, keys in
+// boxes of 128 and of 64 rows, values in boxes of 64
 struct Maps {
-  CUtensorMap q_prefix, q_own, pk, pv, kk, kv, kk32, kv32;
+  CUtensorMap q_prefix, q_own, pk, pk64, pv, kk, kk64, kv;
 };
 
 template <int HD>
@@ -289,126 +289,129 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         at0 += __shfl_sync(0xffffffffu, incl, 31);
       }
     }
-    if (lane == 0) {
-      const uint32_t stages = kside ? C::kKStages : C::kVStages;
-      uint32_t g = 0, tile = 0;
-      bool ok = true;
-      auto load = [&](const Segment& s) {  // the segment's row tiles and blocks
-        const bool own_kind = s.kind & 1;
-        if (kside) {
-          for (int x = 0; x < (s.kind & 2 ? 2 : 1); ++x, ++tile) {
-            const uint32_t use = tile / C::kQTiles;
-            if (use > 0 && !wait(q_empty(tile), (use - 1) & 1)) { ok = false; return; }
-            const int t = 2 * s.item + x;  // row tile
-            const int first = sh.groups > 1 ? t / sh.groups : own_kind ? 0 : t;  // request (of a prefix tile)
-            const CUtensorMap* m = own_kind ? &maps.q_own : &maps.q_prefix;
-            const int r = own_kind ? s.r : first * sh.requests, tok = (sh.groups > 1 ? t - first * sh.groups : 0) * sh.tokens;
-            mbar_expect_tx(q_full(tile), (own_kind ? sh.own_rec : sh.prefix_rec) * HD * 2);
-            for (int c = 0; c < C::kChunks; ++c)
-              tma_tile_4d(sQ + (tile % C::kQTiles) * C::kTileBytes + c * C::kPiece, m, 64 * c, s.head * sh.G, tok, r,
-                          q_full(tile));
-          }
-        }
-        for (int j = 0; j < s.n; ++j, ++g) {
-          const uint32_t use = g / stages;
-          if (use > 0 && !wait(kside ? k_empty(g) : v_empty(g), (use - 1) & 1)) { ok = false; return; }
-          const int key = (s.b0 + j) * kKeys;
-          const uint32_t bar = kside ? k_full(g) : v_full(g);
-          const uint32_t dst = kside ? sK + (g % C::kKStages) * C::kTileBytes : sV + (g % C::kVStages) * C::kTileBytes;
-          if (own_kind && s.keys - key <= kKeys - 32) {  // the last block of a cache, in groups of 32 rows
-            const int n32 = (s.keys - key + 31) / 32;
-            mbar_expect_tx(bar, n32 * 32 * HD * 2);
-            for (int i = 0; i < n32; ++i)
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_tile_4d(kside ? dst + c * C::kPiece + i * 4096 : dst + ((i >> 1) * C::kChunks + c) * 8192 + (i & 1) * 4096,
-                            kside ? &maps.kk32 : &maps.kv32, 64 * c, s.head, key + 32 * i, s.r, bar);
-          } else if (kside) {
-            const CUtensorMap* m = own_kind ? &maps.kk : &maps.pk;
-            mbar_expect_tx(bar, C::kTileBytes);
-            for (int c = 0; c < C::kChunks; ++c) tma_tile_4d(dst + c * C::kPiece, m, 64 * c, s.head, key, s.r, bar);
-          } else {
-            const CUtensorMap* m = own_kind ? &maps.kv : &maps.pv;
-            mbar_expect_tx(bar, C::kTileBytes);
-            for (int half = 0; half < 2; ++half)
-              for (int c = 0; c < C::kChunks; ++c)
-                tma_tile_4d(dst + (half * C::kChunks + c) * 8192, m, 64 * c, s.head, key + 64 * half, s.r, bar);
-          }
-        }
-      };
+    const uint32_t stages = kside ? C::kKStages : C::kVStages;
+    uint32_t g = 0, tile = 0;
+    bool ok = true;
+    auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    // The whole warp walks along; lane 0 announces a copy's bytes and a lane per box issues it.
+    auto load = [&](const Segment& s) {  // the segment's row tiles and blocks
+      const bool own_kind = s.kind & 1;
       if (kside) {
-        uint32_t i = 0;
-        auto publish = [&](const Segment& s) {
-          if (i >= static_cast<uint32_t>(C::kRing) && !wait(seg_empty(i), (i / C::kRing - 1) & 1)) { ok = false; return; }
+        for (int x = 0; x < (s.kind & 2 ? 2 : 1); ++x, ++tile) {
+          const uint32_t use = tile / C::kQTiles;
+          if (use > 0 && !wwait(q_empty(tile), (use - 1) & 1)) { ok = false; return; }
+          const int t = 2 * s.item + x;  // row tile
+          const int first = sh.groups > 1 ? t / sh.groups : own_kind ? 0 : t;  // request (of a prefix tile)
+          const int r = own_kind ? s.r : first * sh.requests, tok = (sh.groups > 1 ? t - first * sh.groups : 0) * sh.tokens;
+          if (lane == 0) mbar_expect_tx(q_full(tile), (own_kind ? sh.own_rec : sh.prefix_rec) * HD * 2);
+          __syncwarp();
+          if (lane < C::kChunks)
+            tma_tile_4d(sQ + (tile % C::kQTiles) * C::kTileBytes + lane * C::kPiece, own_kind ? &maps.q_own : &maps.q_prefix,
+                        64 * lane, s.head * sh.G, tok, r, q_full(tile));
+        }
+      }
+      for (int j = 0; j < s.n; ++j, ++g) {
+        const uint32_t use = g / stages;
+        if (use > 0 && !wwait(kside ? k_empty(g) : v_empty(g), (use - 1) & 1)) { ok = false; return; }
+        const int key = (s.b0 + j) * kKeys;
+        const uint32_t bar = kside ? k_full(g) : v_full(g);
+        const bool half = s.keys - key <= kKeys / 2;  // the first 64 keys are all there are
+        if (lane == 0) mbar_expect_tx(bar, half ? C::kTileBytes / 2 : C::kTileBytes);
+        __syncwarp();
+        if (kside) {  // one box of 128 (64) rows per 64 dimensions
+          const CUtensorMap* m = own_kind ? (half ? &maps.kk64 : &maps.kk) : (half ? &maps.pk64 : &maps.pk);
+          if (lane < C::kChunks)
+            tma_tile_4d(sK + (g % C::kKStages) * C::kTileBytes + lane * C::kPiece, m, 64 * lane, s.head, key, s.r, bar);
+        } else {  // a box of 64 rows per half and 64 dimensions
+          if (lane < (half ? 1 : 2) * C::kChunks)
+            tma_tile_4d(sV + (g % C::kVStages) * C::kTileBytes + lane * 8192, own_kind ? &maps.kv : &maps.pv,
+                        64 * (lane % C::kChunks), s.head, key + 64 * (lane / C::kChunks), s.r, bar);
+        }
+      }
+    };
+    if (kside) {
+      uint32_t i = 0;
+      auto publish = [&](const Segment& s) {
+        if (i >= static_cast<uint32_t>(C::kRing) && !wwait(seg_empty(i), (i / C::kRing - 1) & 1)) { ok = false; return; }
+        if (lane == 0) {
           ring[2 * (i % C::kRing)] = make_int4(s.kind, s.head, s.item, s.r);
           ring[2 * (i % C::kRing) + 1] = make_int4(s.b0, s.n, s.keys, s.rec);
           mbar_arrive1(seg_full(i));
-          ++i;
-          if (s.kind >= 0) load(s);
-        };
-        // the blocks of the item at `at` that start in [from, to)
-        auto cut = [&](long long from, long long to, long long at, int extra, int cost, int blocks, Segment& s) {
-          s.b0 = Deal::before(from, at, extra, cost, blocks);
-          s.n = Deal::before(to, at, extra, cost, blocks) - s.b0;
-          return s.n > 0;
-        };
-        if (cta < shared.n && prefix_total > 0) {
-          const long long from = shared.start(cta), to = shared.start(cta + 1);
-          const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
-          for (int k = static_cast<int>(from / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < to; ++k) {
-            Segment s;
-            s.head = k / sh.prefix_items;
-            s.item = k - s.head * sh.prefix_items;
-            s.kind = 2 * s.item + 1 < sh.prefix_tiles ? 2 : 0;
-            s.r = 0;
-            s.keys = sh.P;
-            s.rec = k + cta;
-            if (cut(from, to, k * cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
+        }
+        ++i;
+        if (s.kind >= 0) load(s);
+      };
+      // the blocks of the item at `at`, of cost `all`, that start in [from, to)
+      auto cut = [&](long long from, long long to, long long at, long long all, int extra, int cost, int blocks, Segment& s) {
+        s.b0 = from <= at ? 0 : Deal::before(from, at, extra, cost, blocks);
+        s.n = (to >= at + all ? blocks : Deal::before(to, at, extra, cost, blocks)) - s.b0;
+        return s.n > 0;
+      };
+      if (cta < shared.n && prefix_total > 0) {
+        const long long from = shared.start(cta), to = shared.start(cta + 1);
+        const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
+        for (int k = static_cast<int>(from / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < to; ++k) {
+          Segment s;
+          s.head = k / sh.prefix_items;
+          s.item = k - s.head * sh.prefix_items;
+          s.kind = 2 * s.item + 1 < sh.prefix_tiles ? 2 : 0;
+          s.r = 0;
+          s.keys = sh.P;
+          s.rec = k + cta;
+          if (cut(from, to, k * cost, cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
+        }
+      }
+      const int per_r = sh.Hkv * sh.own_items;
+      for (int r = r0; ok && r < sh.R && at0 < end; ++r) {
+        const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
+        const long long cost = sh.own_item(nb);
+        if (nb > 0) {
+          int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0;
+          Segment s;
+          s.head = h / sh.own_items;
+          s.item = h - s.head * sh.own_items;
+          s.r = r;
+          s.keys = keys;
+          for (long long at = at0 + h * cost; ok && h < per_r && at < end; ++h, at += cost) {
+            s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
+            s.rec = r * per_r + h + cta;
+            if (cut(pos, end, at, cost, kCostItem, sh.own_cost, nb, s)) publish(s);
+            if (++s.item == sh.own_items) {
+              s.item = 0;
+              ++s.head;
+            }
           }
         }
-        const int per_r = sh.Hkv * sh.own_items;
-        for (int r = r0; ok && r < sh.R && at0 < end; ++r) {
-          const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
-          const long long cost = sh.own_item(nb);
-          if (nb > 0)
-            for (int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0; ok && h < per_r && at0 + h * cost < end; ++h) {
-              Segment s;
-              s.head = h / sh.own_items;
-              s.item = h - s.head * sh.own_items;
-              s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
-              s.r = r;
-              s.keys = keys;
-              s.rec = r * per_r + h + cta;
-              if (cut(pos, end, at0 + h * cost, kCostItem, sh.own_cost, nb, s)) publish(s);
-            }
-          at0 += cost * per_r;
-        }
-        Segment last{};
-        last.kind = -1;
-        if (ok) publish(last);
-      } else {
-        Segment s;
-        for (uint32_t i = 0; ok && read_segment(i, s); ++i) load(s);
+        at0 += cost * per_r;
       }
-      // no copy may still be landing when the CTA leaves (matters only after an abort)
-      for (uint32_t x = g > stages ? g - stages : 0; x < g; ++x)
-        wait_drain(kside ? k_full(x) : v_full(x), (x / stages) & 1, kWaitLimitCycles);
-      if (kside)
-        for (uint32_t x = tile > C::kQTiles ? tile - C::kQTiles : 0; x < tile; ++x)
-          wait_drain(q_full(x), (x / C::kQTiles) & 1, kWaitLimitCycles);
+      Segment last{};
+      last.kind = -1;
+      if (ok) publish(last);
+    } else {
+      Segment s;
+      for (uint32_t i = 0; ok && read_segment_warp(i, s); ++i) load(s);
     }
+    // no copy may still be landing when the CTA leaves (matters only after an abort)
+    for (uint32_t x = g > stages ? g - stages : 0; x < g; ++x)
+      wait_drain(kside ? k_full(x) : v_full(x), (x / stages) & 1, kWaitLimitCycles);
+    if (kside)
+      for (uint32_t x = tile > C::kQTiles ? tile - C::kQTiles : 0; x < tile; ++x)
+        wait_drain(q_full(x), (x / C::kQTiles) & 1, kWaitLimitCycles);
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issuer ----------------
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0);
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
       uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
       uint32_t turn = 0;            // blocks with one row tile so far: the TMEM tile is its parity
       uint32_t ns[2] = {0u, 0u};    // S products issued per TMEM tile
       uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose first P V has been issued
       bool ok = true, any = false;
+      // groups of 16 keys in block b of a segment's item
+      auto groups16 = [&](const Segment& s, int b) { return (min(s.keys - b * kKeys, kKeys) + 15) / 16; };
       // S_x = Q K^T of row tile `qt` and ring block gu; the P that shared its columns was read by a
       // product issued before
-      auto issue_s = [&](int x, uint32_t qt, uint32_t gu) {
+      auto issue_s = [&](int x, uint32_t qt, uint32_t gu, int keys16) {
+        const uint32_t idesc_s = idesc_bf16_f32(kRows, 16 * keys16, 0);
         const uint32_t q_at = sQ + (qt % C::kQTiles) * C::kTileBytes;
         const uint32_t k_at = sK + (gu % C::kKStages) * C::kTileBytes;
 #pragma unroll
@@ -427,7 +430,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         return true;
       };
       // O_x (+)= P_x V of ring block gu, P_x from tile x's last S
-      auto issue_pv = [&](int x, uint32_t gu, bool first) {
+      auto issue_pv = [&](int x, uint32_t gu, int keys16, bool first) {
         if (!wait(p_full(x), (ns[x] - 1) & 1)) return false;
         if (first) {
           if (no[x] > 0 && !wait(o_free(x), (no[x] - 1) & 1)) return false;
@@ -437,6 +440,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k) {
+          if (k >= keys16) break;
           const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
           umma_bf16_ts(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
                        (!first || k > 0) ? 1u : 0u);
@@ -448,12 +452,12 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
       // with one row tile: the product of the block whose S was issued last waits until the
       // next block's S (of the other TMEM tile, of the next segment too) has been issued
       bool pending = false, pending_first = false;
-      int pending_x = 0;
+      int pending_x = 0, pending_keys = 0;
       uint32_t pending_g = 0;
       auto flush = [&]() {
         if (!pending) return true;
         pending = false;
-        if (!wait_v(pending_g) || !issue_pv(pending_x, pending_g, pending_first)) return false;
+        if (!wait_v(pending_g) || !issue_pv(pending_x, pending_g, pending_keys, pending_first)) return false;
         umma_commit(v_empty(pending_g));
         return true;
       };
@@ -465,20 +469,22 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           for (int j = 0; j < n && ok; ++j, ++turn, ++g) {
             const int x = turn & 1;
             if (!wait_k(g)) { ok = false; break; }
-            issue_s(x, tile, g);
+            const int keys16 = groups16(s, s.b0 + j);
+            issue_s(x, tile, g, keys16);
             umma_commit(k_empty(g));
             if (j + 1 == n) umma_commit(q_empty(tile));
             if (!flush()) { ok = false; break; }
             pending = true;
             pending_x = x;
+            pending_keys = keys16;
             pending_g = g;
             pending_first = j < 2;  // the segment's first block on this TMEM tile
           }
           ++tile;
         } else {
           if (!flush() || !wait_q(tile) || !wait_q(tile + 1) || !wait_k(g)) { ok = false; break; }
-          issue_s(0, tile, g);
-          issue_s(1, tile + 1, g);
+          issue_s(0, tile, g, groups16(s, s.b0));
+          issue_s(1, tile + 1, g, groups16(s, s.b0));
           umma_commit(k_empty(g));
           for (int j = 0; j < n && ok; ++j) {
             const uint32_t gu = g + j;
@@ -488,10 +494,10 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
             }
             if (!wait_v(gu)) { ok = false; break; }
             for (int x = 0; x < 2 && ok; ++x) {
-              if (!issue_pv(x, gu, j == 0)) { ok = false; break; }
+              if (!issue_pv(x, gu, groups16(s, s.b0 + j), j == 0)) { ok = false; break; }
               if (j + 1 < n) {
                 if (x == 0 && !wait_k(gu + 1)) { ok = false; break; }
-                issue_s(x, tile + x, gu + 1);
+                issue_s(x, tile + x, gu + 1, groups16(s, s.b0 + j + 1));
               }
             }
             if (!ok) break;
@@ -543,10 +549,10 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         tc_fence_after();
         const int jb = j0 + j * step;
         const int key0 = (s.b0 + jb) * kKeys;
-        if (own && s.keys - key0 < kKeys && (!two || x == 0)) {  // V rows past the end of the request's cache
+        if (own && ((s.keys - key0) & 15) && s.keys - key0 < kKeys && (!two || x == 0)) {  // V rows past the end of the cache
           const uint32_t gu = g + jb;
           if (!wwait(v_full(gu), (gu / C::kVStages) & 1)) { ok = false; break; }
-          if (row >= s.keys - key0) {
+          if (row >= s.keys - key0 && row < (s.keys - key0 + 15) / 16 * 16) {
             uint8_t* v = smem + C::kOffV + (gu % C::kVStages) * C::kTileBytes + (row >> 6) * (C::kChunks * 8192) + (row & 63) * 128;
             for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
@@ -836,12 +842,12 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
       !row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1))
     return MTP_ERR_CUDA;
   if (p.P > 0 && (!row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, kKeys, 1) ||
+                  !row_map(&m.pk64, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1) ||
                   !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
     return MTP_ERR_CUDA;
   if (p.T > 0 && (!row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, kKeys, 1) ||
                   !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1) ||
-                  !row_map(&m.kk32, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 32, 1) ||
-                  !row_map(&m.kv32, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 32, 1)))
+                  !row_map(&m.kk64, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1)))
     return MTP_ERR_CUDA;
   const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
   if (p.P > 0 || p.T > 0) {
