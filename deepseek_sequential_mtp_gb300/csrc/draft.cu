@@ -23,7 +23,10 @@
 // kernel turns into probabilities in place and samples from.
 // With the module's linear maps in FP8 block-scaled form (mtp_draft_round_fp8)
 // the same products run on the FP8 weight GEMM of fp8.cu, which streams half
-// the bytes; the head stays bf16.
+// the bytes, in 4 bits (mtp_draft_round_ext) on that of int4.cu, a quarter; the
+// head stays bf16.  Cache rows that all requests share (a common prompt) are
+// kept once and read once: the attention over a prefix runs as its own kernel
+// (prefix_attn.cu) and leaves one more record per (request, head).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -33,7 +36,9 @@
 #include "decode_gemm.cuh"
 #include "fp8.cuh"
 #include "gemm_tc.cuh"
+#include "int4.cuh"
 #include "mbarrier.cuh"
+#include "prefix_attn.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -335,7 +340,7 @@ template <int HD>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 decode_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const __nv_bfloat16* __restrict__ qkv, const int32_t* __restrict__ ctx_len,
-                   float* __restrict__ part, int H, int T, int n_split, int split_keys, int n_units, float scale) {
+                   float* __restrict__ part, int H, int T, int n_split, int n_rec, int split_keys, int n_units, float scale) {
   using C = AttnCfg<HD>;
   constexpr int S = C::kStages;
   constexpr int kKSteps = HD / 16;  // score MMAs per 8 keys
@@ -538,7 +543,7 @@ decode_attn_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constan
           O += e * s_o[b][w][threadIdx.x];
         }
       }
-      float* rec = part + ((static_cast<size_t>(r) * H + h) * n_split + sp) * (HD + 2);
+      float* rec = part + ((static_cast<size_t>(r) * H + h) * n_rec + sp) * (HD + 2);
       if (threadIdx.x == 0) {
         rec[0] = M;
         rec[1] = L;
@@ -819,13 +824,13 @@ inline size_t align_up(size_t v) { return (v + 255) & ~static_cast<size_t>(255);
 constexpr int kMaxRoundGamma = 31;  // draft steps per round (spec_verify takes gamma <= 31)
 
 struct DraftLayout {
-  size_t c, acc, u, x, qkv, o, a, g, h, part, stage_k, stage_v, f8ws, f8ws_bytes, total;
+  size_t c, acc, u, x, qkv, o, a, g, h, part, stage_k, stage_v, f8ws, f8ws_bytes, prefix_ws, prefix_ws_bytes, total;
   int n_chunks;
 };
 
 // h holds two [R, d] rows (the state of the step and of the previous one);
 // stage_k / stage_v hold the rotated key and the value of every step's row
-DraftLayout draft_layout(const mtp_dims& D, int gamma) {
+DraftLayout draft_layout(const mtp_dims& D, int gamma, int prefix_len) {
   DraftLayout L{};
   const size_t R = D.B, d = D.d;
   L.n_chunks = std::max(1, (D.T + kAttnSplitKeys - 1) / kAttnSplitKeys);
@@ -845,12 +850,16 @@ DraftLayout draft_layout(const mtp_dims& D, int gamma) {
   L.a = take(R * d * 2);
   L.g = take(R * static_cast<size_t>(D.ffn) * 2);
   L.h = take(2 * R * d * 2);
-  L.part = take(R * static_cast<size_t>(D.n_heads) * L.n_chunks * (D.head_dim + 2) * 4);
+  L.part = take(R * static_cast<size_t>(D.n_heads) * (L.n_chunks + (prefix_len > 0 ? 1 : 0)) * (D.head_dim + 2) * 4);
   L.stage_k = take(R * static_cast<size_t>(gamma) * d * 2);
   L.stage_v = take(R * static_cast<size_t>(gamma) * d * 2);
   // the FP8 linear maps' split activations (largest reduction length: 2d or ffn)
   L.f8ws_bytes = mtp::fp8w_workspace_bytes(std::max(2 * D.d, D.ffn));
   L.f8ws = take(L.f8ws_bytes);
+  if (prefix_len > 0) {
+    L.prefix_ws_bytes = mtp::prefix_attn_workspace_bytes(D.B, 1, D.n_heads, D.n_heads, D.head_dim, prefix_len, 0);
+    L.prefix_ws = take(L.prefix_ws_bytes);
+  }
   L.total = off;
   return L;
 }
@@ -901,7 +910,7 @@ namespace {
 // and the frontier token (stride f_stride), writes the step's state h_s (row
 // stride ld_h), logits/q into q_s (row stride ldq), the draw into y_s (stride
 // y_stride) and the step's key/value into staging slot s.
-mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_block_fp8* f8, const DraftLayout& L,
+mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_draft_ext& ext, const DraftLayout& L,
                           uint8_t* base,
                           const __nv_bfloat16* parent, int ld_parent, const int32_t* frontier, int f_stride,
                           const int32_t* pos, const void* kv_k, const void* kv_v, const int32_t* ctx_len, int step,
@@ -914,15 +923,32 @@ mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_blo
   const __nv_bfloat16* E = static_cast<const __nv_bfloat16*>(w->embed);
   __nv_bfloat16 *c = bfp(L.c), *u = bfp(L.u), *x = bfp(L.x), *qkv = bfp(L.qkv), *o = bfp(L.o), *a = bfp(L.a),
                 *g = bfp(L.g), *sk = bfp(L.stage_k), *sv = bfp(L.stage_v);
-  // acc[:, col + (0..n)] += xin · W^T for one to three linear maps of the
+  // acc[:, col + (0..n)] = xin · W^T for one to three linear maps of the
   // block that share their input, in one grouped launch: bf16 weights on the
-  // decode GEMM (decode_gemm.cu), FP8 block-scaled ones on the FP8 GEMM
+  // decode GEMM (decode_gemm.cu), FP8 block-scaled ones on the FP8 GEMM, 4-bit ones on int4.cu's
   struct Map {
     const void* const* bf;
     const mtp_fp8_matrix* q8;
+    const mtp_int4_matrix* q4;
     int n, col;
   };
+  const mtp_block_fp8* f8 = ext.fp8;
+  const mtp_block_int4* i4 = ext.int4;
   auto linear = [&](std::initializer_list<Map> maps, int K, const __nv_bfloat16* xin, int ldo) -> mtp_status {
+    if (i4) {  // writes acc, where the others add to it
+      mtp::Int4Seg segs[3];
+      int i = 0;
+      for (const Map& m : maps) {
+        segs[i].q = static_cast<const uint8_t*>(m.q4->q);
+        segs[i].scale = static_cast<const __nv_bfloat16*>(m.q4->scale);
+        segs[i].zero = static_cast<const uint8_t*>(m.q4->zero);
+        segs[i].n = m.n;
+        segs[i].out = acc + m.col;
+        ++i;
+      }
+      return mtp::int4w_gemm_launch(segs, i, K, i4->group, xin, R, ldo, false, st);
+    }
+    MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * ldo * 4, st));
     if (f8) {
       mtp::Fp8Seg segs[3];
       int i = 0;
@@ -945,24 +971,23 @@ mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_blo
     }
     return mtp::dgemm_bf16_launch(segs, i, K, xin, R, ldo, st);
   };
-  auto q8 = [&](const mtp_fp8_matrix mtp_block_fp8::*field) { return f8 ? &(f8->*field) : nullptr; };
+  auto map = [&](const void* const* bf, const mtp_fp8_matrix mtp_block_fp8::*q8, const mtp_int4_matrix mtp_block_int4::*q4,
+                 int n, int col) { return Map{bf, f8 ? &(f8->*q8) : nullptr, i4 ? &(i4->*q4) : nullptr, n, col}; };
 
   // c, u = M c, x = RMSNorm_a(u)
   draft_prologue_kernel<<<R, kRowThreads, 0, st>>>(parent, ld_parent, frontier, f_stride, E, W0(w->hnorm),
                                                    W0(w->enorm), c, d, V, D.eps);
   mtp::note_launch();
-  MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * d * 4, st));
-  TRY(linear({{w->eh_proj, q8(&mtp_block_fp8::eh_proj), d, 0}}, 2 * d, c, d));
+  TRY(linear({map(w->eh_proj, &mtp_block_fp8::eh_proj, &mtp_block_int4::eh_proj, d, 0)}, 2 * d, c, d));
   finish_row_kernel<<<R, kRowThreads, 0, st>>>(acc, nullptr, u, d, W0(w->attn_norm), x, d, D.eps);
   mtp::note_launch();
   // q, k, v with RoPE on q, k at pos + step; the row's k, v staged in slot `step`
-  MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * 3 * d * 4, st));
-  TRY(linear({{w->wq, q8(&mtp_block_fp8::wq), d, 0},
-              {w->wk, q8(&mtp_block_fp8::wk), d, d},
-              {w->wv, q8(&mtp_block_fp8::wv), d, 2 * d}},
+  TRY(linear({map(w->wq, &mtp_block_fp8::wq, &mtp_block_int4::wq, d, 0),
+              map(w->wk, &mtp_block_fp8::wk, &mtp_block_int4::wk, d, d),
+              map(w->wv, &mtp_block_fp8::wv, &mtp_block_int4::wv, d, 2 * d)},
              d, x, 3 * d));
   finish_qkv_kernel<<<dim3((d + kQkvCols - 1) / kQkvCols, R), 256, 0, st>>>(acc, qkv, pos, step, d, hd, D.rope_base,
-                                                                            D.T, sk, sv, gamma);
+                                                                            D.T + ext.prefix_len, sk, sv, gamma);
   mtp::note_launch();
   // attention over the module's own cache, the rows staged by earlier steps and the new row
   const float scale = 1.0f / sqrtf(static_cast<float>(hd));
@@ -972,6 +997,7 @@ mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_blo
   const int n_split = L.n_chunks;
   const int split_keys = ((D.T + n_split - 1) / n_split + kAttnTileKeys - 1) / kAttnTileKeys * kAttnTileKeys;
   const int n_units = R * H * n_split;
+  const int n_rec = n_split + (ext.prefix_len > 0 ? 1 : 0);
   const int agrid = std::min(n_units, sm_count());
   CUtensorMap tmk, tmv;
   const uint64_t cache_rows = static_cast<uint64_t>(R) * D.T;
@@ -980,39 +1006,53 @@ mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_blo
       !mtp::tensor_map_bf16_2d(&tmv, vc, cache_rows, d, d, 64, kAttnTileKeys, true))
     return MTP_ERR_CUDA;
   mtp::prof_begin(MTP_KC_ATTENTION, st);
+  if (ext.prefix_len > 0) {  // the rows that all requests share, as the last record of each (request, head)
+    mtp::PrefixAttn pa;
+    pa.R = R;
+    pa.H = pa.Hkv = H;
+    pa.hd = hd;
+    pa.P = ext.prefix_len;
+    pa.scale = scale;
+    pa.q = qkv;
+    pa.q_r = pa.q_l = 3ll * d;
+    pa.q_h = pa.p_h = hd;
+    pa.pk = static_cast<const __nv_bfloat16*>(ext.prefix_k);
+    pa.pv = static_cast<const __nv_bfloat16*>(ext.prefix_v);
+    pa.p_t = d;
+    pa.rec = part + static_cast<size_t>(n_split) * (hd + 2);
+    pa.rec_stride = static_cast<long long>(n_rec) * (hd + 2);
+    TRY(mtp::prefix_attn_launch(pa, base + L.prefix_ws, L.prefix_ws_bytes, st));
+  }
   if (hd == 128) {
     static mtp::PerDevice attr;
     if (!mtp::smem_limit(attr, decode_attn_kernel<128>, AttnCfg<128>::kSmemBytes)) return MTP_ERR_CUDA;
     decode_attn_kernel<128><<<agrid, kAttnThreads, AttnCfg<128>::kSmemBytes, st>>>(
-        tmk, tmv, qkv, ctx_len, part, H, D.T, n_split, split_keys, n_units, scale);
+        tmk, tmv, qkv, ctx_len, part, H, D.T, n_split, n_rec, split_keys, n_units, scale);
     mtp::note_launch();
     decode_attn_combine_kernel<128><<<(R * H + 7) / 8, 256, 0, st>>>(qkv, sk, sv, gamma, step + 1, part, o, R, H,
-                                                                     n_split, scale);
+                                                                     n_rec, scale);
   } else {
     static mtp::PerDevice attr;
     if (!mtp::smem_limit(attr, decode_attn_kernel<64>, AttnCfg<64>::kSmemBytes)) return MTP_ERR_CUDA;
     decode_attn_kernel<64><<<agrid, kAttnThreads, AttnCfg<64>::kSmemBytes, st>>>(
-        tmk, tmv, qkv, ctx_len, part, H, D.T, n_split, split_keys, n_units, scale);
+        tmk, tmv, qkv, ctx_len, part, H, D.T, n_split, n_rec, split_keys, n_units, scale);
     mtp::note_launch();
     decode_attn_combine_kernel<64><<<(R * H + 7) / 8, 256, 0, st>>>(qkv, sk, sv, gamma, step + 1, part, o, R, H,
-                                                                    n_split, scale);
+                                                                    n_rec, scale);
   }
   mtp::note_launch();
   mtp::prof_end(MTP_KC_ATTENTION, st);
   // a = u + o Wo^T, x = RMSNorm_f(a)
-  MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * d * 4, st));
-  TRY(linear({{w->wo, q8(&mtp_block_fp8::wo), d, 0}}, d, o, d));
+  TRY(linear({map(w->wo, &mtp_block_fp8::wo, &mtp_block_int4::wo, d, 0)}, d, o, d));
   finish_row_kernel<<<R, kRowThreads, 0, st>>>(acc, u, a, d, W0(w->ffn_norm), x, d, D.eps);
   mtp::note_launch();
   // g = silu(x Wg^T) * (x Wu^T)
-  MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * 2 * ffn * 4, st));
-  TRY(linear({{w->w_gate, q8(&mtp_block_fp8::w_gate), ffn, 0}, {w->w_up, q8(&mtp_block_fp8::w_up), ffn, ffn}}, d, x,
+  TRY(linear({map(w->w_gate, &mtp_block_fp8::w_gate, &mtp_block_int4::w_gate, ffn, 0), map(w->w_up, &mtp_block_fp8::w_up, &mtp_block_int4::w_up, ffn, ffn)}, d, x,
              2 * ffn));
   finish_swiglu_kernel<<<dim3((ffn + 255) / 256, R), 256, 0, st>>>(acc, g, ffn);
   mtp::note_launch();
   // h = a + g Wd^T, x = RMSNorm_out(h)
-  MTP_CUDA_TRY(cudaMemsetAsync(acc, 0, static_cast<size_t>(R) * d * 4, st));
-  TRY(linear({{w->w_down, q8(&mtp_block_fp8::w_down), d, 0}}, ffn, g, d));
+  TRY(linear({map(w->w_down, &mtp_block_fp8::w_down, &mtp_block_int4::w_down, d, 0)}, ffn, g, d));
   finish_row_kernel<<<R, kRowThreads, 0, st>>>(acc, a, h_s, ld_h, static_cast<const __nv_bfloat16*>(w->out_norm),
                                                x, d, D.eps);
   mtp::note_launch();
@@ -1033,14 +1073,19 @@ mtp_status draft_one_step(const mtp_dims& D, const mtp_weights* w, const mtp_blo
 
 extern "C" size_t mtp_draft_round_workspace_bytes(const mtp_dims* dims, int gamma) {
   if (!dims || !draft_dims_ok(*dims) || gamma < 1 || gamma > kMaxRoundGamma) return 0;
-  return draft_layout(*dims, gamma).total;
+  return draft_layout(*dims, gamma, 0).total;
+}
+
+extern "C" size_t mtp_draft_round_ext_workspace_bytes(const mtp_dims* dims, int gamma, int prefix_len) {
+  if (!dims || !draft_dims_ok(*dims) || gamma < 1 || gamma > kMaxRoundGamma || prefix_len < 0) return 0;
+  return draft_layout(*dims, gamma, prefix_len).total;
 }
 
 extern "C" size_t mtp_draft_workspace_bytes(const mtp_dims* dims) { return mtp_draft_round_workspace_bytes(dims, 1); }
 
 namespace {
 
-mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mtp_block_fp8* f8,
+mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mtp_draft_ext& ext,
                             const void* parent_hidden, const int32_t* frontier, const int32_t* pos, const void* kv_k,
                             const void* kv_v, const int32_t* ctx_len, int gamma, uint64_t seed, uint64_t offset,
                             float* q_out, int32_t* y_out, void* h_out, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -1055,7 +1100,24 @@ mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mt
   const void* const* norms[] = {w->hnorm, w->enorm, w->attn_norm, w->ffn_norm};
   for (auto l : norms)
     if (!l || !l[0] || !mtp::aligned16(l[0])) return l && l[0] ? MTP_ERR_ALIGNMENT : MTP_ERR_INVALID_ARG;
-  if (f8) {
+  const mtp_block_fp8* f8 = ext.fp8;
+  const mtp_block_int4* i4 = ext.int4;
+  if (f8 && i4) return MTP_ERR_INVALID_ARG;
+  if (ext.prefix_len < 0) return MTP_ERR_INVALID_ARG;
+  if (ext.prefix_len > 0) {
+    if (!ext.prefix_k || !ext.prefix_v) return MTP_ERR_INVALID_ARG;
+    if (!mtp::aligned16(ext.prefix_k) || !mtp::aligned16(ext.prefix_v)) return MTP_ERR_ALIGNMENT;
+  }
+  if (i4) {
+    if (D.ffn % 32) return MTP_ERR_UNSUPPORTED;  // 16-byte rows of the down projection's codes
+    if (i4->group != 32 && i4->group != 64 && i4->group != 128) return MTP_ERR_UNSUPPORTED;
+    const mtp_int4_matrix* mats[] = {&i4->eh_proj, &i4->wq, &i4->wk, &i4->wv, &i4->wo,
+                                     &i4->w_gate, &i4->w_up, &i4->w_down};
+    for (auto m : mats) {
+      if (!m->q || !m->scale) return MTP_ERR_INVALID_ARG;
+      if (!mtp::aligned16(m->q) || (reinterpret_cast<uintptr_t>(m->scale) & 1u)) return MTP_ERR_ALIGNMENT;
+    }
+  } else if (f8) {
     if (D.ffn % 16) return MTP_ERR_UNSUPPORTED;  // 16-byte rows of the e4m3 down projection
     const mtp_fp8_matrix* mats[] = {&f8->eh_proj, &f8->wq, &f8->wk, &f8->wv, &f8->wo,
                                     &f8->w_gate, &f8->w_up, &f8->w_down};
@@ -1073,7 +1135,7 @@ mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mt
   for (const void* p : ptrs)
     if (!mtp::aligned16(p)) return MTP_ERR_ALIGNMENT;
   if (h_out && !mtp::aligned16(h_out)) return MTP_ERR_ALIGNMENT;
-  const DraftLayout L = draft_layout(D, gamma);
+  const DraftLayout L = draft_layout(D, gamma, ext.prefix_len);
   if (ws_bytes < L.total) return MTP_ERR_WORKSPACE;
 
   const int R = D.B, d = D.d;
@@ -1097,7 +1159,7 @@ mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mt
       f = y_out + (s - 1);
       f_stride = gamma;
     }
-    TRY(draft_one_step(D, w, f8, L, base, parent, ld_parent, f, f_stride, pos, kv_k, kv_v, ctx_len, s, gamma, key,
+    TRY(draft_one_step(D, w, ext, L, base, parent, ld_parent, f, f_stride, pos, kv_k, kv_v, ctx_len, s, gamma, key,
                        offset, q_out + static_cast<size_t>(s) * D.V, ldq, y_out + s, gamma, h_s, ld_h, st));
   }
   return MTP_OK;
@@ -1110,7 +1172,7 @@ extern "C" mtp_status mtp_draft_round(const mtp_dims* dims, const mtp_weights* w
                                       const void* kv_v, const int32_t* ctx_len, int gamma, uint64_t seed,
                                       uint64_t offset, float* q_out, int32_t* y_out, void* h_out, void* ws,
                                       size_t ws_bytes, cudaStream_t st) {
-  return draft_round_impl(dims, w, nullptr, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, gamma, seed, offset,
+  return draft_round_impl(dims, w, mtp_draft_ext{}, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, gamma, seed, offset,
                           q_out, y_out, h_out, ws, ws_bytes, st);
 }
 
@@ -1120,8 +1182,19 @@ extern "C" mtp_status mtp_draft_round_fp8(const mtp_dims* dims, const mtp_weight
                                           uint64_t seed, uint64_t offset, float* q_out, int32_t* y_out, void* h_out,
                                           void* ws, size_t ws_bytes, cudaStream_t st) {
   if (!f8) return MTP_ERR_INVALID_ARG;
-  return draft_round_impl(dims, w, f8, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, gamma, seed, offset, q_out,
+  mtp_draft_ext ext{};
+  ext.fp8 = f8;
+  return draft_round_impl(dims, w, ext, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, gamma, seed, offset, q_out,
                           y_out, h_out, ws, ws_bytes, st);
+}
+
+extern "C" mtp_status mtp_draft_round_ext(const mtp_dims* dims, const mtp_weights* w, const mtp_draft_ext* ext,
+                                          const void* parent_hidden, const int32_t* frontier, const int32_t* pos,
+                                          const void* kv_k, const void* kv_v, const int32_t* ctx_len, int gamma,
+                                          uint64_t seed, uint64_t offset, float* q_out, int32_t* y_out, void* h_out,
+                                          void* ws, size_t ws_bytes, cudaStream_t st) {
+  return draft_round_impl(dims, w, ext ? *ext : mtp_draft_ext{}, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, gamma,
+                          seed, offset, q_out, y_out, h_out, ws, ws_bytes, st);
 }
 
 extern "C" mtp_status mtp_draft_step(const mtp_dims* dims, const mtp_weights* w, const void* parent_hidden,

@@ -64,6 +64,15 @@ class Int4Matrix(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p)]
 
 
+class BlockInt4(ctypes.Structure):
+    _fields_ = [(k, Int4Matrix) for k in FP8_LINEAR_MAPS] + [("group", ctypes.c_int)]
+
+
+class DraftExt(ctypes.Structure):
+    _fields_ = [("fp8", ctypes.POINTER(BlockFp8)), ("int4", ctypes.POINTER(BlockInt4)),
+                ("prefix_k", ctypes.c_void_p), ("prefix_v", ctypes.c_void_p), ("prefix_len", ctypes.c_int)]
+
+
 class PrefixDims(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int) for k in ("R", "L", "n_heads", "n_kv_heads", "head_dim", "P", "T", "causal")] + \
                [("scale", ctypes.c_float)] + \
@@ -126,6 +135,12 @@ def load() -> ctypes.CDLL:
                                    u64, u64, vp, vp, vp, vp, sz, vp]
     lib.mtp_draft_round_fp8.restype = i32
     lib.mtp_draft_round_fp8.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(Weights), ctypes.POINTER(BlockFp8),
+                                        vp, vp, vp, vp, vp, vp, i32, ctypes.c_uint64, ctypes.c_uint64, vp, vp, vp,
+                                        vp, sz, vp]
+    lib.mtp_draft_round_ext_workspace_bytes.restype = sz
+    lib.mtp_draft_round_ext_workspace_bytes.argtypes = [ctypes.POINTER(Dims), i32, i32]
+    lib.mtp_draft_round_ext.restype = i32
+    lib.mtp_draft_round_ext.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(Weights), ctypes.POINTER(DraftExt),
                                         vp, vp, vp, vp, vp, vp, i32, ctypes.c_uint64, ctypes.c_uint64, vp, vp, vp,
                                         vp, sz, vp]
     lib.mtp_gemm_decode_bf16.restype = i32
@@ -390,6 +405,24 @@ class Fp8Block:
             m.scale = sc.data_ptr()
 
 
+class Int4Block:
+    """ctypes view of the 4-bit linear maps of one module: int4[name] = (q, scale,
+    zero or None) as _int4_matrix takes them."""
+
+    def __init__(self, int4: dict, group: int, cfg):
+        d, f = cfg.d, cfg.ffn
+        self.int4 = int4
+        self.struct = BlockInt4()
+        self.struct.group = int(group)
+        shapes = {"eh_proj": (d, 2 * d), "w_gate": (f, d), "w_up": (f, d), "w_down": (d, f)}
+        for name in FP8_LINEAR_MAPS:
+            q, sc, z = int4[name]
+            n, k = shapes.get(name, (d, d))
+            if tuple(q.shape) != (n, k // 2):
+                raise MtpError(f"{name}.q must be [{n}, {k // 2}]")
+            setattr(self.struct, name, _int4_matrix(name, q, sc, z, int(group), q.device))
+
+
 def gemm_decode_bf16(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, stream=None):
     """out[R, N] += x[R, K] @ w[N, K]^T for R <= 32 tokens (mtp_gemm_decode_bf16)."""
     _need(x, "x", torch.bfloat16)
@@ -639,74 +672,28 @@ def kernel_launches() -> int:
 # --------------------------------------------------------------------------
 # Draft step (decode-shaped MTP proposal)
 # --------------------------------------------------------------------------
-class DraftStep:
-    """Reusable call state of mtp_draft_step for one shape (see synth.DraftConfig)."""
+class _Draft:
+    """Call state of a draft round of ``gamma`` steps for one shape: dims, weight
+    views, workspace."""
 
-    def __init__(self, cfg, weights: dict, device="cuda", fp8: Optional[dict] = None):
-        self.cfg = cfg
-        self.dims = Dims(cfg.R, cfg.ctx, cfg.d, cfg.n_heads, cfg.head_dim, cfg.ffn, cfg.V, 1, cfg.eps,
-                         cfg.rope_base, MTP_BF16)
-        self.weights = weights
-        self.w = ChainWeights(weights, 1)
-        self.f8 = Fp8Block(fp8) if fp8 is not None else None
-        nbytes = int(load().mtp_draft_workspace_bytes(ctypes.byref(self.dims)))
-        if nbytes == 0:
-            raise MtpError("invalid draft-step dimensions")
-        self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
-                 out=None, h_out=None, stream=None):
-        cfg = self.cfg
-        _need(parent_hidden, "parent_hidden", torch.bfloat16)
-        for name, t in (("kv_k", kv_k), ("kv_v", kv_v)):
-            _need(t, name, torch.bfloat16)
-            if tuple(t.shape) != (cfg.R, cfg.ctx, cfg.d):
-                raise MtpError(f"{name} must be [R, ctx, d]")
-        for name, t in (("frontier", frontier), ("pos", pos), ("ctx_len", ctx_len)):
-            _need(t, name, torch.int32)
-        dev = parent_hidden.device
-        if out is None:
-            out = {"q": torch.empty((cfg.R, cfg.V), dtype=torch.float32, device=dev),
-                   "y": torch.empty(cfg.R, dtype=torch.int32, device=dev)}
-        if self.f8 is not None:  # one step of the FP8 round
-            st = load().mtp_draft_round_fp8(ctypes.byref(self.dims), ctypes.byref(self.w.struct),
-                                            ctypes.byref(self.f8.struct), _ptr(parent_hidden), _ptr(frontier),
-                                            _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len), 1,
-                                            int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]),
-                                            _ptr(out["y"]), _ptr(h_out), _ptr(self.ws), self.ws.numel(),
-                                            _stream(stream))
-            _check(st, "mtp_draft_round_fp8")
-        else:
-            st = load().mtp_draft_step(ctypes.byref(self.dims), ctypes.byref(self.w.struct), _ptr(parent_hidden),
-                                       _ptr(frontier), _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len),
-                                       int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]),
-                                       _ptr(out["y"]), _ptr(h_out), _ptr(self.ws), self.ws.numel(),
-                                       _stream(stream))
-            _check(st, "mtp_draft_step")
-        if h_out is not None:
-            out["h"] = h_out
-        return out
-
-
-class DraftRound:
-    """Reusable call state of mtp_draft_round: gamma recurrent draft steps of
-    one module for one shape (see synth.DraftConfig)."""
-
-    def __init__(self, cfg, weights: dict, gamma: int, device="cuda", fp8: Optional[dict] = None):
+    def __init__(self, cfg, weights: dict, gamma: int, device, fp8, int4, int4_group, prefix_len):
         self.cfg = cfg
         self.gamma = int(gamma)
+        self.prefix_len = int(prefix_len)
         self.dims = Dims(cfg.R, cfg.ctx, cfg.d, cfg.n_heads, cfg.head_dim, cfg.ffn, cfg.V, 1, cfg.eps,
                          cfg.rope_base, MTP_BF16)
         self.weights = weights
         self.w = ChainWeights(weights, 1)
+        if fp8 is not None and int4 is not None:
+            raise MtpError("a module has its linear maps in FP8 or in 4 bits, not both")
         self.f8 = Fp8Block(fp8) if fp8 is not None else None
-        nbytes = int(load().mtp_draft_round_workspace_bytes(ctypes.byref(self.dims), self.gamma))
+        self.i4 = Int4Block(int4, int4_group, cfg) if int4 is not None else None
+        nbytes = int(load().mtp_draft_round_ext_workspace_bytes(ctypes.byref(self.dims), self.gamma, self.prefix_len))
         if nbytes == 0:
-            raise MtpError("invalid draft-round dimensions or gamma")
+            raise MtpError("invalid draft-step dimensions or gamma")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
 
-    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
-                 out=None, h_out=None, stream=None):
+    def run(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream, prefix_k, prefix_v):
         cfg, g = self.cfg, self.gamma
         _need(parent_hidden, "parent_hidden", torch.bfloat16)
         for name, t in (("kv_k", kv_k), ("kv_v", kv_v)):
@@ -715,6 +702,73 @@ class DraftRound:
                 raise MtpError(f"{name} must be [R, ctx, d]")
         for name, t in (("frontier", frontier), ("pos", pos), ("ctx_len", ctx_len)):
             _need(t, name, torch.int32)
+        ext = None
+        if self.i4 is not None or self.prefix_len > 0:
+            ext = DraftExt()
+            if self.f8 is not None:
+                ext.fp8 = ctypes.pointer(self.f8.struct)
+            if self.i4 is not None:
+                ext.int4 = ctypes.pointer(self.i4.struct)
+            if self.prefix_len > 0:
+                for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)):
+                    if t is None:
+                        raise MtpError(f"{name} is missing")
+                    _arg(t, name, torch.bfloat16, (self.prefix_len, cfg.d), parent_hidden.device)
+                ext.prefix_k, ext.prefix_v, ext.prefix_len = prefix_k.data_ptr(), prefix_v.data_ptr(), self.prefix_len
+        if self.prefix_len == 0 and (prefix_k is not None or prefix_v is not None):
+            raise MtpError("prefix rows were given to a draft step built with prefix_len = 0")
+        rows = (_ptr(parent_hidden), _ptr(frontier), _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len))
+        rest = (int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]), _ptr(out["y"]), _ptr(h_out),
+                _ptr(self.ws), self.ws.numel(), _stream(stream))
+        dims, w = ctypes.byref(self.dims), ctypes.byref(self.w.struct)
+        if ext is not None:
+            _check(load().mtp_draft_round_ext(dims, w, ctypes.byref(ext), *rows, g, *rest), "mtp_draft_round_ext")
+        elif self.f8 is not None:
+            _check(load().mtp_draft_round_fp8(dims, w, ctypes.byref(self.f8.struct), *rows, g, *rest),
+                   "mtp_draft_round_fp8")
+        elif isinstance(self, DraftStep):
+            _check(load().mtp_draft_step(dims, w, *rows, *rest), "mtp_draft_step")
+        else:
+            _check(load().mtp_draft_round(dims, w, *rows, g, *rest), "mtp_draft_round")
+        if h_out is not None:
+            out["h"] = h_out
+        return out
+
+
+class DraftStep(_Draft):
+    """Reusable call state of mtp_draft_step for one shape (see synth.DraftConfig).
+    The module's linear maps may be in FP8 (``fp8``) or in 4 bits (``int4``:
+    name -> (q, scale, zero or None), groups of ``int4_group``), and the caches
+    may begin with ``prefix_len`` rows that all requests share, passed to each
+    call as prefix_k and prefix_v [prefix_len, d] (mtp_draft_round_ext)."""
+
+    def __init__(self, cfg, weights: dict, device="cuda", fp8: Optional[dict] = None, int4: Optional[dict] = None,
+                 int4_group: int = 128, prefix_len: int = 0):
+        super().__init__(cfg, weights, 1, device, fp8, int4, int4_group, prefix_len)
+
+    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
+                 out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
+        cfg = self.cfg
+        dev = parent_hidden.device
+        if out is None:
+            out = {"q": torch.empty((cfg.R, cfg.V), dtype=torch.float32, device=dev),
+                   "y": torch.empty(cfg.R, dtype=torch.int32, device=dev)}
+        return self.run(parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream,
+                        prefix_k, prefix_v)
+
+
+class DraftRound(_Draft):
+    """Reusable call state of mtp_draft_round: gamma recurrent draft steps of
+    one module for one shape (see synth.DraftConfig).  ``fp8``, ``int4`` and
+    ``prefix_len`` as for DraftStep."""
+
+    def __init__(self, cfg, weights: dict, gamma: int, device="cuda", fp8: Optional[dict] = None,
+                 int4: Optional[dict] = None, int4_group: int = 128, prefix_len: int = 0):
+        super().__init__(cfg, weights, gamma, device, fp8, int4, int4_group, prefix_len)
+
+    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
+                 out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
+        cfg, g = self.cfg, self.gamma
         if h_out is not None:
             _need(h_out, "h_out", torch.bfloat16)
             if tuple(h_out.shape) != (cfg.R, g, cfg.d):
@@ -723,24 +777,8 @@ class DraftRound:
         if out is None:
             out = {"q": torch.empty((cfg.R, g, cfg.V), dtype=torch.float32, device=dev),
                    "y": torch.empty((cfg.R, g), dtype=torch.int32, device=dev)}
-        if self.f8 is not None:
-            st = load().mtp_draft_round_fp8(ctypes.byref(self.dims), ctypes.byref(self.w.struct),
-                                            ctypes.byref(self.f8.struct), _ptr(parent_hidden), _ptr(frontier),
-                                            _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len), g,
-                                            int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]),
-                                            _ptr(out["y"]), _ptr(h_out), _ptr(self.ws), self.ws.numel(),
-                                            _stream(stream))
-            _check(st, "mtp_draft_round_fp8")
-        else:
-            st = load().mtp_draft_round(ctypes.byref(self.dims), ctypes.byref(self.w.struct), _ptr(parent_hidden),
-                                        _ptr(frontier), _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len), g,
-                                        int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]),
-                                        _ptr(out["y"]), _ptr(h_out), _ptr(self.ws), self.ws.numel(),
-                                        _stream(stream))
-            _check(st, "mtp_draft_round")
-        if h_out is not None:
-            out["h"] = h_out
-        return out
+        return self.run(parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream,
+                        prefix_k, prefix_v)
 
 
 # --------------------------------------------------------------------------

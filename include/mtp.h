@@ -490,18 +490,6 @@ mtp_status mtp_draft_round_fp8(const mtp_dims* dims, const mtp_weights* w, const
                                uint64_t seed, uint64_t offset, float* q_out, int32_t* y_out, void* h_out,
                                void* ws, size_t ws_bytes, cudaStream_t stream);
 
-/* Bytes of device workspace mtp_gemm_fp8w needs for reduction length K. */
-size_t mtp_gemm_fp8w_workspace_bytes(int K);
-
-/* Diagnostic FP8 weight GEMM (the kernel the FP8 draft step uses):
- * out[R, N] (fp32, row stride N) += x~[R, K] · W^T with W the FP8
- * block-scaled matrix (wq [N, K] e4m3, scale [ceil(N/128), ceil(K/128)]) and
- * x~ the two-term e4m3 form of x (bf16) described at mtp_fp8_matrix.
- * R in [1, 32], K % 16 == 0, x and wq 16-byte aligned; ws: at least
- * mtp_gemm_fp8w_workspace_bytes(K) bytes of device memory, 16-byte aligned. */
-mtp_status mtp_gemm_fp8w(int R, int N, int K, const void* x, const void* wq, const float* scale, float* out,
-                         void* ws, size_t ws_bytes, cudaStream_t stream);
-
 /* One 4-bit weight matrix W [n, K] with group scales:
  *   W[m][k] = (code[m][k] - zero[m][k/group]) * scale[m][k/group], taken exactly.
  * q: [n, K/2] bytes, row-major, 16-byte aligned; byte j of a row holds code 2j
@@ -514,6 +502,54 @@ typedef struct mtp_int4_matrix {
   const void* scale;
   const void* zero;
 } mtp_int4_matrix;
+
+/* The linear maps of one MTP module in 4 bits (shapes as in mtp_weights), all
+ * with the same group size: 32, 64 or 128. */
+typedef struct mtp_block_int4 {
+  mtp_int4_matrix eh_proj, wq, wk, wv, wo, w_gate, w_up, w_down;
+  int group;
+} mtp_block_int4;
+
+/* What a draft round may have besides mtp_draft_round's arguments; zero
+ * members leave it as it is.
+ *   fp8, int4 (at most one): the module's linear maps in that form; w's are not
+ *   read then and may be null.  int4 requires ffn % 32 == 0.
+ *   prefix_k, prefix_v [prefix_len, d] bf16, 16-byte aligned: keys and values, as
+ *   the cache holds them, of rows that precede every request's own cache (a
+ *   prompt that the batch shares).  They are kept and read once for the batch;
+ *   the result is that of caches which begin with these rows, to the rounding of
+ *   the prefix's softmax weights to bf16.  pos may reach T + prefix_len. */
+typedef struct mtp_draft_ext {
+  const mtp_block_fp8* fp8;
+  const mtp_block_int4* int4;
+  const void* prefix_k;
+  const void* prefix_v;
+  int prefix_len;
+} mtp_draft_ext;
+
+/* Bytes of device workspace mtp_draft_round_ext needs on the current device (0
+ * if the sizes are invalid). */
+size_t mtp_draft_round_ext_workspace_bytes(const mtp_dims* dims, int gamma, int prefix_len);
+
+/* mtp_draft_round with `ext` (nullable).  Everything else, including the
+ * outputs and the random stream, is as for mtp_draft_round. */
+mtp_status mtp_draft_round_ext(const mtp_dims* dims, const mtp_weights* w, const mtp_draft_ext* ext,
+                               const void* parent_hidden, const int32_t* frontier, const int32_t* pos,
+                               const void* kv_k, const void* kv_v, const int32_t* ctx_len, int gamma,
+                               uint64_t seed, uint64_t offset, float* q_out, int32_t* y_out, void* h_out,
+                               void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace mtp_gemm_fp8w needs for reduction length K. */
+size_t mtp_gemm_fp8w_workspace_bytes(int K);
+
+/* Diagnostic FP8 weight GEMM (the kernel the FP8 draft step uses):
+ * out[R, N] (fp32, row stride N) += x~[R, K] · W^T with W the FP8
+ * block-scaled matrix (wq [N, K] e4m3, scale [ceil(N/128), ceil(K/128)]) and
+ * x~ the two-term e4m3 form of x (bf16) described at mtp_fp8_matrix.
+ * R in [1, 32], K % 16 == 0, x and wq 16-byte aligned; ws: at least
+ * mtp_gemm_fp8w_workspace_bytes(K) bytes of device memory, 16-byte aligned. */
+mtp_status mtp_gemm_fp8w(int R, int N, int K, const void* x, const void* wq, const float* scale, float* out,
+                         void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Product of 1..32 tokens with a 4-bit weight matrix (the kernel the draft
  * step uses with 4-bit weights): out[R, N] (fp32, row stride N) = x[R, K] · W^T,

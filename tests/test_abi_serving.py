@@ -75,3 +75,39 @@ def test_prefix_attention_host_validation(lib):
     assert call(q=ODD) == 3 and call(lse=ODD) == 3 and call(ctx=ODD) == 3 and call(q_stride_h=68) == 3
     assert call(kv_stride_t=-8) == 2
     assert call(ws_bytes=64) == 4
+
+
+def test_draft_round_ext_host_validation(lib):
+    from deepseek_sequential_mtp_gb300 import lib as binding, synth
+    cfg = synth.DRAFT_SMALL
+    dims = binding.Dims(cfg.R, cfg.ctx, cfg.d, cfg.n_heads, cfg.head_dim, cfg.ffn, cfg.V, 1, cfg.eps,
+                        cfg.rope_base, binding.MTP_BF16)
+    one = (ctypes.c_void_p * 1)(1 << 20)
+    w = binding.Weights()
+    w.embed = w.head = w.out_norm = 1 << 20
+    for k in binding._WEIGHT_LISTS:
+        setattr(w, k, ctypes.cast(one, binding._PP))
+
+    def call(ws_bytes=16, **kw):
+        ext = binding.DraftExt()
+        for k, v in kw.items():
+            setattr(ext, k, v)
+        return lib.mtp_draft_round_ext(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(ext), *[FAKE] * 6, 1, 0, 0,
+                                       FAKE, FAKE, None, FAKE, ws_bytes, None)
+
+    def int4(group=64, q=1 << 20, scale=1 << 20):
+        b = binding.BlockInt4()
+        b.group = group
+        for k in binding.FP8_LINEAR_MAPS:
+            setattr(b, k, binding.Int4Matrix(q, scale, None))
+        return ctypes.pointer(b)
+
+    assert call() == 4 and call(int4=int4()) == 4 and call(prefix_len=5, prefix_k=1 << 20, prefix_v=1 << 20) == 4
+    assert call(prefix_len=-1) == 1 and call(prefix_len=5) == 1 and call(prefix_len=5, prefix_k=1 << 20) == 1
+    assert call(prefix_len=5, prefix_k=(1 << 20) + 8, prefix_v=1 << 20) == 3
+    assert call(int4=int4(group=16)) == 7 and call(int4=int4(q=None)) == 1 and call(int4=int4(q=(1 << 20) + 4)) == 3
+    assert call(int4=int4(scale=(1 << 20) + 1)) == 3
+    assert call(int4=int4(), fp8=ctypes.pointer(binding.BlockFp8())) == 1
+    size = lambda g, p: lib.mtp_draft_round_ext_workspace_bytes(ctypes.byref(dims), g, p)  # noqa: E731
+    assert size(2, 0) == lib.mtp_draft_round_workspace_bytes(ctypes.byref(dims), 2) and size(2, 500) > size(2, 0)
+    assert size(0, 0) == 0 and size(32, 0) == 0 and size(1, -1) == 0
