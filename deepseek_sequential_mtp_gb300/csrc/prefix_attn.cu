@@ -162,10 +162,10 @@ struct Cfg {
   static constexpr uint32_t kColO = 256;
 };
 
-// tensor maps: q in boxes of a prefix tile's and of an own tile's rows, keys in
-// boxes of 128 and of 64 rows, values in boxes of 64
+// tensor maps: q in boxes of a prefix tile's and of an own tile's rows, keys and
+// values in boxes of 64 rows
 struct Maps {
-  CUtensorMap q_prefix, q_own, pk, pk64, pv, kk, kk64, kv;
+  CUtensorMap q_prefix, q_own, pk, pv, kk, kv;
 };
 
 template <int HD>
@@ -318,14 +318,12 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         const bool half = s.keys - key <= kKeys / 2;  // the first 64 keys are all there are
         if (lane == 0) mbar_expect_tx(bar, half ? C::kTileBytes / 2 : C::kTileBytes);
         __syncwarp();
-        if (kside) {  // one box of 128 (64) rows per 64 dimensions
-          const CUtensorMap* m = own_kind ? (half ? &maps.kk64 : &maps.kk) : (half ? &maps.pk64 : &maps.pk);
-          if (lane < C::kChunks)
-            tma_tile_4d(sK + (g % C::kKStages) * C::kTileBytes + lane * C::kPiece, m, 64 * lane, s.head, key, s.r, bar);
-        } else {  // a box of 64 rows per half and 64 dimensions
-          if (lane < (half ? 1 : 2) * C::kChunks)
-            tma_tile_4d(sV + (g % C::kVStages) * C::kTileBytes + lane * 8192, own_kind ? &maps.kv : &maps.pv,
-                        64 * (lane % C::kChunks), s.head, key + 64 * (lane / C::kChunks), s.r, bar);
+        if (lane < (half ? 1 : 2) * C::kChunks) {  // a box per 64 rows and 64 dimensions
+          const int rows64 = lane / C::kChunks, c = lane % C::kChunks;
+          const uint32_t dst = kside ? sK + (g % C::kKStages) * C::kTileBytes + c * C::kPiece + rows64 * 8192
+                                     : sV + (g % C::kVStages) * C::kTileBytes + lane * 8192;
+          const CUtensorMap* m = kside ? (own_kind ? &maps.kk : &maps.pk) : (own_kind ? &maps.kv : &maps.pv);
+          tma_tile_4d(dst, m, 64 * c, s.head, key + 64 * rows64, s.r, bar);
         }
       }
     };
@@ -838,16 +836,15 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   static PerDevice attr;
   if (!smem_limit(attr, prefix_attn_kernel<HD>, C::kSmemBytes)) return MTP_ERR_CUDA;
   Maps m{};
-  if (!row_map(&m.q_prefix, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, s.requests) ||
-      !row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1))
+  if (p.P > 0 &&
+      (!row_map(&m.q_prefix, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, s.requests) ||
+       !row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1) ||
+       !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
     return MTP_ERR_CUDA;
-  if (p.P > 0 && (!row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, kKeys, 1) ||
-                  !row_map(&m.pk64, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1) ||
-                  !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
-    return MTP_ERR_CUDA;
-  if (p.T > 0 && (!row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, kKeys, 1) ||
-                  !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1) ||
-                  !row_map(&m.kk64, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1)))
+  if (p.T > 0 &&
+      (!row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1) ||
+       !row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1) ||
+       !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1)))
     return MTP_ERR_CUDA;
   const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
   if (p.P > 0 || p.T > 0) {

@@ -185,7 +185,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without the object around it (3 us of a small call), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -203,10 +209,10 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device
     """Address of an optional dense argument of the given type, shape and device (None = null)."""
     if t is None:
         return None
-    _need(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise MtpError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _need(t, name, dtype)
+        if tuple(t.shape) != tuple(shape):
+            raise MtpError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         raise MtpError(f"{name} is on {t.device}, not on {device}")
     return t.data_ptr()
 
@@ -222,7 +228,7 @@ def _launch_device(t: torch.Tensor, stream):
 
 def _empty(shape, dtype, device, stream):
     """An output or workspace whose memory belongs to the launching stream."""
-    if stream is None:
+    if stream is None or stream == torch.cuda.current_stream():
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -784,11 +790,14 @@ class DraftRound(_Draft):
 # --------------------------------------------------------------------------
 # Attention over a shared prefix
 # --------------------------------------------------------------------------
+_DENSE = {n: (0,) * (n - 1) for n in range(1, 9)}
+
+
 def _strides(t: torch.Tensor, name: str):
-    """Strides of all dimensions but the last, which has to be dense; 0 (of no
-    consequence) for those of one element."""
-    if t.numel() == 0:
-        return [0] * (t.dim() - 1)
+    """Strides of all dimensions but the last, which has to be dense; 0 for those
+    of a dense tensor, and (of no consequence) for those of one element."""
+    if t.is_contiguous():
+        return _DENSE[t.dim()]
     if t.stride(-1) != 1:
         raise MtpError(f"{name} must be dense in its last dimension")
     if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
@@ -798,11 +807,13 @@ def _strides(t: torch.Tensor, name: str):
 
 def _pair(k, v, name: str, dims: int, device):
     """Keys and values of one shape and layout, the last dimension dense."""
-    for n, t in ((name + "_k", k), (name + "_v", v)):
-        if t.dim() != dims or t.dtype != torch.bfloat16 or t.device != device:
-            raise MtpError(f"{n} must be a bfloat16 tensor of {dims} dimensions on {device}")
-    if k.shape != v.shape or _strides(k, name + "_k") != _strides(v, name + "_v"):
+    for t in (k, v):
+        if t.dim() != dims or t.dtype is not torch.bfloat16 or t.device != device:
+            raise MtpError(f"{name}_k and {name}_v must be bfloat16 tensors of {dims} dimensions on {device}")
+    strides = _strides(k, name + "_k")
+    if k.shape != v.shape or strides != _strides(v, name + "_v"):
         raise MtpError(f"{name}_k and {name}_v must have the same shape and strides")
+    return strides
 
 
 def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Tensor,
@@ -819,7 +830,7 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
         raise MtpError("q must be bfloat16 [R, L, H, hd]")
     dev = _launch_device(q, stream)
     R, L, H, hd = q.shape
-    _pair(prefix_k, prefix_v, "prefix", 3, dev)
+    prefix_strides = _pair(prefix_k, prefix_v, "prefix", 3, dev)
     P, Hkv = prefix_k.shape[0], prefix_k.shape[1]
     if prefix_k.shape[2] != hd:
         raise MtpError("prefix_k must be [P, Hkv, hd]")
@@ -827,15 +838,15 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     if scale is not None and not 0.0 < scale < 3e38:
         raise MtpError("scale must be positive and finite")
     d.q_stride_r, d.q_stride_t, d.q_stride_h = _strides(q, "q")
-    d.prefix_stride_t, d.prefix_stride_h = _strides(prefix_k, "prefix_k")
+    d.prefix_stride_t, d.prefix_stride_h = prefix_strides
     if (kv_k is None) != (kv_v is None):
         raise MtpError("kv_k and kv_v come together")
     if kv_k is not None:
-        _pair(kv_k, kv_v, "kv", 4, dev)
+        kv_strides = _pair(kv_k, kv_v, "kv", 4, dev)
         if kv_k.shape[0] != R or tuple(kv_k.shape[2:]) != (Hkv, hd):
             raise MtpError("kv_k must be [R, T, Hkv, hd]")
         d.T = kv_k.shape[1]
-        d.kv_stride_r, d.kv_stride_t, d.kv_stride_h = _strides(kv_k, "kv_k")
+        d.kv_stride_r, d.kv_stride_t, d.kv_stride_h = kv_strides
     elif ctx_len is not None:
         raise MtpError("ctx_len needs kv_k and kv_v")
     ctx = _arg(ctx_len, "ctx_len", torch.int32, (R,), dev)
