@@ -10,7 +10,7 @@
 // most 32 of 128 columns are tokens.  e4m3 operands, for which a code is its
 // own byte, unpack in 3 instructions a word instead of 11, but mma.sync
 // executes them on this machine as two bf16-rate products after 17 more
-// instructions: 93 us instead of 54 on 7168 x 18432 with 32 tokens.)
+// instructions: 93 us instead of 43 on 7168 x 18432 with 32 tokens.)
 //
 // The sum over k may be taken in any order, so a lane feeds the fragments
 // straight from its own 16 bytes: the quad that shares a weight row reads 64
@@ -45,10 +45,12 @@ constexpr int kUnitBytes = 2 * kChunk;  // a token's activations of one chunk
 constexpr int kPitchPad = 64;           // two token rows' units fall into different banks
 constexpr int kMaxTokens = 32;
 
-// Variants by the number of 8-token tiles NT.
+// Variants by the number of 8-token tiles NT: with more than one, one CTA of 16
+// warps per SM shares the staged activations (16 tokens, 18432 x 7168: 28 us;
+// two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47), with one, three of 8.
 template <int NT> struct Cfg {
-  static constexpr int kWarps = 8;
-  static constexpr int kCtas = NT == 4 ? 2 : 3;   // per SM
+  static constexpr int kWarps = NT > 1 ? 16 : 8;
+  static constexpr int kCtas = NT > 1 ? 1 : 3;      // per SM
   static constexpr int kDepth = 4;  // chunks of weights in flight per warp
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlotBytes = 2 * 32 * 16;          // a warp's chunk: 16 bytes per lane and row
@@ -409,14 +411,14 @@ mtp_status plan(Args& a, const mtp::Int4Seg* segs, int group, cudaStream_t st) {
   // every SM.  Up to 4 tokens: the largest tile that does so without a split
   // (18432 x 7168, one token: 64 rows 20.7 us, 128 rows on two CTAs 22.6, 16
   // rows 24.7); more tokens: the largest that does so with one (8 tokens: 128
-  // rows on two CTAs 25 us, 64 rows 29; 32 tokens, 7168 x 18432: 128 rows on
-  // four CTAs 54 us, 64 rows 90).
+  // rows on two CTAs 25 us, 64 rows 29).  Then k is split over as many CTAs as
+  // the SMs hold at once (32 tokens, 7168 x 18432: 43 us on 5, 51 on 4, 56 on 8).
   const int sms = mtp::sm_count_current();
   auto tiles_of = [&](int w) { return (n_all + 16 * w - 1) / (16 * w); };
   int wm = F::kWarps;
   while (wm > 1 && tiles_of(wm) * (a.R > 4 ? 8 : 1) < sms) wm /= 2;
-  int C = 1;
-  while (C < 8 && tiles_of(wm) * C * 2 < 3 * sms && a.chunks / (2 * C) >= F::kWarps / wm) C *= 2;
+  int C = 8;
+  while (C > 1 && (tiles_of(wm) * C > static_cast<long long>(sms) * F::kCtas || a.chunks / C < F::kWarps / wm)) --C;
   const int wk = F::kWarps / wm, bm = 16 * wm;
   a.wm = wm;
   a.cta_chunks = (a.chunks + C - 1) / C;
