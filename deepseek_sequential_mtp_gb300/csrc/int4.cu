@@ -22,7 +22,7 @@
 // memory in the same order: within 8 neighbours 0 4 1 5 2 6 3 7, and the four
 // lanes' 16-byte units side by side, so the B fragments are conflict-free
 // 16-byte reads.  All lanes of a quad have to be in one group of k while they
-// accumulate: a chunk of 128 weights is 128/G groups, and lane t takes
+// accumulate: 128 weights are 128/G groups, and lane t takes
 // 32 consecutive weights of one group (G = 128), 16 of each of two (64) or
 // 8 of each of four (32), with 16-, 8- or 4-byte copies.
 //
@@ -40,8 +40,6 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kChunk = 128;             // weights of a row per step
-constexpr int kUnitBytes = 2 * kChunk;  // a token's activations of one chunk
 constexpr int kPitchPad = 64;           // two token rows' units fall into different banks
 constexpr int kMaxTokens = 32;
 
@@ -49,11 +47,14 @@ constexpr int kMaxTokens = 32;
 // warps per SM shares the staged activations (16 tokens, 18432 x 7168: 28 us;
 // two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47), with one, three of 8.
 template <int NT> struct Cfg {
+  static constexpr int kChunk = NT > 1 ? 128 : 256;       // weights of a row per step
+  static constexpr int kUnitBytes = 2 * kChunk;           // a token's activations of one chunk
+  static constexpr int kWords = kChunk / 32;              // words of a row per lane
   static constexpr int kWarps = NT > 1 ? 16 : 8;
-  static constexpr int kCtas = NT > 1 ? 1 : 3;      // per SM
+  static constexpr int kCtas = NT > 1 ? 1 : 2;      // per SM
   static constexpr int kDepth = 4;  // chunks of weights in flight per warp
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kSlotBytes = 2 * 32 * 16;          // a warp's chunk: 16 bytes per lane and row
+  static constexpr int kSlotBytes = kChunk * 8;           // a warp's chunk: 16 bytes per lane, row and 128 weights
   static constexpr int kRingSlots = kDepth <= 4 ? 4 : 8;  // a power of two: slots by mask
   static constexpr int kRingBytes = kWarps * kRingSlots * kSlotBytes;
   static constexpr int kSmem = (kCtas == 1 ? 224 : kCtas == 2 ? 112 : kCtas == 3 ? 74 : 55) * 1024;
@@ -71,7 +72,7 @@ struct Args {
   Seg seg[3];
   int nseg, R, K, groups, ldo, accumulate;
   int wm;            // warps along the rows
-  int chunks;        // chunks of 128 along K
+  int chunks;        // chunks along K
   int cta_chunks;    // ... per CTA of the cluster
   int piece_chunks;  // ... of activations staged at a time
   int by4;           // groups are a multiple of 4 from 8-byte boundaries on: staged four at a time
@@ -91,7 +92,7 @@ __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -109,7 +110,8 @@ __device__ __forceinline__ uint32_t unpack(uint32_t w, int i, uint32_t z) {
 // first weight (within a chunk) of word w of lane t of the quad
 template <int G>
 __device__ __forceinline__ int word_k(int w, int t) {
-  return G == 128 ? 32 * t + 8 * w : G == 64 ? 64 * (w >> 1) + 16 * t + 8 * (w & 1) : 32 * w + 8 * t;
+  const int v = w & 3;
+  return 128 * (w >> 2) + (G == 128 ? 32 * t + 8 * v : G == 64 ? 64 * (v >> 1) + 16 * t + 8 * (v & 1) : 32 * v + 8 * t);
 }
 
 template <int BYTES>
@@ -121,16 +123,16 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool i
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(n) : "memory");
 }
 
-// a lane's four words of one weight row and chunk (p: the row's bytes of the
-// chunk plus the lane's own offset) into its 16 bytes at dst; of the last
-// chunk only the `valid` weights that there are
+// a lane's four words of 128 weights of a row (p: their bytes plus the lane's
+// own offset) into its 16 bytes at dst; of the last ones only the `valid`
+// weights that there are (p is not read where there are none)
 template <int G, bool WHOLE>
-__device__ __forceinline__ void fetch_words(uint32_t dst, const uint8_t* p, int t, int valid) {
+__device__ __forceinline__ void fetch_words(uint32_t dst, const uint8_t* p, const uint8_t* q, int t, int valid) {
   constexpr int kBytes = G == 128 ? 16 : G == 64 ? 8 : 4;  // as word_k: pieces 4 kBytes apart
 #pragma unroll
   for (int i = 0; i < 16 / kBytes; ++i) {
     const bool in = WHOLE || word_k<G>(i * kBytes / 4, t) < valid;
-    copy_async<kBytes>(dst + i * kBytes, in ? p + 4 * kBytes * i : p - kBytes * t, in);
+    copy_async<kBytes>(dst + i * kBytes, in ? p + 4 * kBytes * i : q, in);
   }
 }
 
@@ -182,7 +184,8 @@ template <int NT, int G>
 __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) int4w_gemm_kernel(const __grid_constant__ Args a) {
   using F = Cfg<NT>;
   constexpr int kWarps = F::kWarps, kThreads = F::kThreads, kDepth = F::kDepth;
-  constexpr int kG = kChunk / G, kPer = 4 / kG;  // groups per chunk, words per group
+  constexpr int kChunk = F::kChunk, kUnitBytes = F::kUnitBytes, kWords = F::kWords;
+  constexpr int kG = kChunk / G, kPer = kWords / kG;  // groups per chunk, words per group
   extern __shared__ __align__(16) uint8_t smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -213,8 +216,12 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) int4w_gemm_
       const int valid = a.K - next * kChunk;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (valid >= kChunk) fetch_words<G, true>(to + h * 512, rows[h], t, valid);
-        else fetch_words<G, false>(to + h * 512, rows[h], t, valid);
+#pragma unroll
+        for (int b = 0; b < kChunk / 128; ++b) {
+          const uint32_t dst = to + (h * (kChunk / 128) + b) * 512;
+          if (valid >= kChunk) fetch_words<G, true>(dst, rows[h] + 64 * b, s.q, t, kChunk);
+          else fetch_words<G, false>(dst, rows[h] + 64 * b, s.q, t, valid - 128 * b);
+        }
         rows[h] += row_step;
       }
     }
@@ -277,13 +284,13 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) int4w_gemm_
     }
     // unit u of a token's chunk holds word u / 4 of lane u % 4; zeros past the end of K
     stage<4, uint4>(
-        kThreads, a.R, (p1 - p0) * 16,
+        kThreads, a.R, (p1 - p0) * 4 * kWords,
         [&](int r, int u) {
-          const int k = (p0 + (u >> 4)) * kChunk + word_k<G>((u >> 2) & 3, u & 3);
+          const int k = (p0 + u / (4 * kWords)) * kChunk + word_k<G>((u >> 2) % kWords, u & 3);
           return __ldg(reinterpret_cast<const uint4*>(a.x + static_cast<size_t>(r) * a.K + min(k, a.K - 8)));
         },
         [&](int r, int u, uint4 v) {
-          if ((p0 + (u >> 4)) * kChunk + word_k<G>((u >> 2) & 3, u & 3) >= a.K) v = make_uint4(0, 0, 0, 0);
+          if ((p0 + u / (4 * kWords)) * kChunk + word_k<G>((u >> 2) % kWords, u & 3) >= a.K) v = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint4*>(xs + r * pitch + u * 16) =
               make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
                          __byte_perm(v.y, v.w, 0x7632));  // 0 4 1 5 2 6 3 7
@@ -295,14 +302,21 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) int4w_gemm_
       fetch(slot_addr(done + kDepth - 1));
       asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
       const uint32_t from = slot_addr(done++);
-      const uint4 qa = lds128(from), qb = lds128(from + 512);
       uint32_t f[2][kG];
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
         f[0][i] = lds32(szt[0] + sz_at + i * 4);
         f[1][i] = lds32(szt[1] + sz_at + i * 4);
       }
-      const uint32_t q[2][4] = {{qa.x, qa.y, qa.z, qa.w}, {qb.x, qb.y, qb.z, qb.w}};
+      uint32_t q[2][kWords];
+#pragma unroll
+      for (int e = 0; e < 2 * kWords / 4; ++e) {
+        const uint4 u = lds128(from + 512 * e);
+        q[e / (kWords / 4)][4 * e % kWords] = u.x;
+        q[e / (kWords / 4)][4 * e % kWords + 1] = u.y;
+        q[e / (kWords / 4)][4 * e % kWords + 2] = u.z;
+        q[e / (kWords / 4)][4 * e % kWords + 3] = u.w;
+      }
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
         float acc[NT][4];
@@ -377,8 +391,8 @@ __global__ void __launch_bounds__(Cfg<NT>::kThreads, Cfg<NT>::kCtas) int4w_gemm_
 // shared memory of a piece: ring, scales, activations
 template <int NT>
 int piece_bytes(int R, int bm, int chunks, int group) {
-  return Cfg<NT>::kRingBytes + (bm * (chunks * (kChunk / group) + 1) * 4 + 15) / 16 * 16 +
-         R * (chunks * kUnitBytes + kPitchPad);
+  using F = Cfg<NT>;
+  return F::kRingBytes + (bm * (chunks * (F::kChunk / group) + 1) * 4 + 15) / 16 * 16 + R * (chunks * F::kUnitBytes + kPitchPad);
 }
 
 template <int NT, int G>
@@ -404,6 +418,7 @@ mtp_status launch(const Args& a, int tiles, int C, int smem, cudaStream_t st) {
 template <int NT>
 mtp_status plan(Args& a, const mtp::Int4Seg* segs, int group, cudaStream_t st) {
   using F = Cfg<NT>;
+  a.chunks = (a.K + F::kChunk - 1) / F::kChunk;
   long long n_all = 0;
   for (int i = 0; i < a.nseg; ++i) n_all += segs[i].n;
   // Rows per CTA and CTAs per cluster.  A large tile stages fewer activations
@@ -428,7 +443,7 @@ mtp_status plan(Args& a, const mtp::Int4Seg* segs, int group, cudaStream_t st) {
   const int smem = std::max(piece_bytes<NT>(a.R, bm, a.piece_chunks, group), wk * a.R * bm * 4);
   if (smem > F::kSmem) return MTP_ERR_UNSUPPORTED;  // not reached: one round fits for every R
   long long tiles = 0;
-  a.by4 = a.groups % 4 == 0 && a.cta_chunks * (kChunk / group) % 4 == 0 && a.piece_chunks * (kChunk / group) % 4 == 0;
+  a.by4 = a.groups % 4 == 0 && a.cta_chunks * (F::kChunk / group) % 4 == 0 && a.piece_chunks * (F::kChunk / group) % 4 == 0;
   for (int i = 0; i < a.nseg; ++i) {
     if ((reinterpret_cast<uintptr_t>(segs[i].scale) & 7u) || (reinterpret_cast<uintptr_t>(segs[i].zero) & 3u)) a.by4 = 0;
     a.seg[i] = Seg{segs[i].q, segs[i].scale, segs[i].zero, segs[i].out, segs[i].n, static_cast<int>(tiles)};
@@ -457,7 +472,6 @@ mtp_status int4w_gemm_launch(const Int4Seg* segs, int nseg, int K, int group, co
   a.ldo = ldo;
   a.accumulate = accumulate;
   a.x = x;
-  a.chunks = (K + kChunk - 1) / kChunk;
   for (int i = 0; i < nseg; ++i)
     if (segs[i].n < 1) return MTP_ERR_SHAPE;
   return R <= 8 ? plan<1>(a, segs, group, st) : R <= 16 ? plan<2>(a, segs, group, st) : plan<4>(a, segs, group, st);
