@@ -57,12 +57,11 @@ constexpr float kStaleMaxLog2 = 8.0f;  // a running maximum is replaced only whe
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 // costs for the deal: a block with one row tile, with two, and what a segment
 // of a request's own cache costs besides
-#ifndef PF_ONE
-#define PF_ONE 6
-#define PF_TWO 11
-#define PF_SEG 5
-#endif
-constexpr int kCostOne = PF_ONE, kCostTwo = PF_TWO, kCostItem = PF_SEG;
+constexpr int kCostOne = 6, kCostTwo = 11, kCostItem = 5;
+// own caches of requests with up to kSmallRows rows per key head have a kernel of
+// their own, with blocks of 64 keys
+constexpr int kSmallBox = 32;  // ... brought in boxes of 32
+constexpr int kSmallRows = 32, kSmallShift = 6, kSmallCost = 2, kSmallCostItem = 1;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -86,7 +85,9 @@ struct Shape {
   int groups;        // token groups per request: ceil(L / tokens)
   int requests;      // requests per row tile of the prefix
   int prefix_tiles, prefix_items, prefix_blocks, prefix_cost;  // row tiles and items per key head; blocks; cost of one
-  int own_items, own_cost;  // row tiles of an own item: `groups` per key head
+  int own_items, own_cost, own_extra;  // row tiles of an own item: `groups` per key head; cost of a block, of an item besides
+  int own_shift, own_ctas;  // log2 of an own block's keys; CTAs that share the own caches
+  int small;                // row tiles of 16 of the small-row kernel, 0: own caches are the prefix kernel's too
   int prefix_rec, own_rec;  // record rows per row tile
   long long own_rec0;       // record row of the first own segment
   int grid;
@@ -97,26 +98,27 @@ struct Shape {
   __host__ __device__ long long prefix_total() const {
     return static_cast<long long>(Hkv) * prefix_items * prefix_blocks * prefix_cost;
   }
-  // cost of an item over `blocks` blocks of an own cache, and of all such items of the request
-  __host__ __device__ long long own_item(int blocks) const {
-    return blocks > 0 ? static_cast<long long>(blocks) * own_cost + kCostItem : 0;
+  // blocks of a request's own cache, cost of an item over them, and of all such items of the request
+  __device__ __forceinline__ int own_blocks(int r) const { return (ctx(r) + (1 << own_shift) - 1) >> own_shift; }
+  __device__ __forceinline__ long long own_item(int blocks) const {
+    return blocks > 0 ? static_cast<long long>(blocks) * own_cost + own_extra : 0;
   }
-  __host__ __device__ long long own_total(int blocks) const { return own_item(blocks) * Hkv * own_items; }
+  __device__ __forceinline__ long long own_total(int blocks) const { return own_item(blocks) * Hkv * own_items; }
 };
 
 // A deal of the prefix's blocks, and one of the own caches': CTA k takes the
 // blocks that start in [k total / n, (k + 1) total / n), n so small that every
-// CTA gets a block.  The first block of an own item costs kCostItem more.  Every
+// CTA gets a block.  The first block of an own item costs own_extra more.  Every
 // CTA works on the prefix first and then on own caches: in one deal over both,
 // the CTAs on the prefix kept the memory queues full, and those on short own
 // items waited 6 us for each of their loads.
 struct Deal {
   long long total;
   int n;
-  __device__ __forceinline__ Deal(const Shape& s, long long total_, int most_cost) {
+  __device__ __forceinline__ Deal(long long total_, int most_cost, int ctas) {
     total = total_;
     const long long most = total / most_cost;
-    n = static_cast<int>(most < 1 ? 1 : most < s.grid ? most : s.grid);
+    n = static_cast<int>(most < 1 ? 1 : most < ctas ? most : ctas);
   }
   __device__ __forceinline__ long long start(int k) const { return k * total / n; }
   // the CTA whose range the position is in
@@ -138,6 +140,75 @@ struct Segment {
   int rec;          // index of its records among the kind's
 };
 static_assert(sizeof(Segment) == 32, "two 16-byte words in the ring");
+
+// The part of the own caches' deal that CTA `cta` takes, walked by a warp.
+struct OwnWalk {
+  long long pos, end, at0;  // its range; where request r0, which the range starts in, starts
+  int r0, cta;
+  __device__ __forceinline__ OwnWalk(const Shape& sh, int cta_, int lane) : at0(0), r0(0), cta(cta_) {
+    long long own = 0;
+    for (int r = lane; r < sh.R; r += 32) own += sh.own_total(sh.own_blocks(r));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    const Deal each(own, sh.own_cost + sh.own_extra, sh.own_ctas);
+    pos = cta < each.n ? each.start(cta) : 0;
+    end = cta < each.n ? each.start(cta + 1) : 0;
+    if (end <= pos) return;
+    for (int base = 0; base < sh.R; base += 32) {
+      const long long c = base + lane < sh.R ? sh.own_total(sh.own_blocks(base + lane)) : 0;
+      long long incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > pos);
+      if (over) {
+        const int src = __ffs(over) - 1;
+        r0 = base + src;
+        at0 += __shfl_sync(0xffffffffu, incl - c, src);
+        return;
+      }
+      at0 += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // take(segment) for each segment, until it returns false
+  template <typename Take>
+  __device__ __forceinline__ bool each_segment(const Shape& sh, Take take) const {
+    const int per_r = sh.Hkv * sh.own_items;
+    long long start = at0;
+    for (int r = r0; r < sh.R && start < end; ++r) {
+      const int keys = sh.ctx(r), nb = sh.own_blocks(r);
+      const long long cost = sh.own_item(nb);
+      if (nb > 0) {
+        int h = pos > start ? static_cast<int>((pos - start) / cost) : 0;
+        Segment s;
+        s.head = h / sh.own_items;
+        s.item = h - s.head * sh.own_items;
+        s.r = r;
+        s.keys = keys;
+        for (long long at = start + h * cost; h < per_r && at < end; ++h, at += cost) {
+          s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
+          s.rec = r * per_r + h + cta;
+          if (cut(pos, end, at, cost, sh.own_extra, sh.own_cost, nb, s) && !take(s)) return false;
+          if (++s.item == sh.own_items) {
+            s.item = 0;
+            ++s.head;
+          }
+        }
+      }
+      start += cost * per_r;
+    }
+    return true;
+  }
+  // the blocks of the item at `at`, of cost `all`, that start in [from, to)
+  static __device__ __forceinline__ bool cut(long long from, long long to, long long at, long long all, int extra, int cost,
+                                             int blocks, Segment& s) {
+    s.b0 = from <= at ? 0 : Deal::before(from, at, extra, cost, blocks);
+    s.n = (to >= at + all ? blocks : Deal::before(to, at, extra, cost, blocks)) - s.b0;
+    return s.n > 0;
+  }
+};
 
 template <int HD>
 struct Cfg {
@@ -259,36 +330,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
   if (warp == C::kKWarp || warp == C::kVWarp) {
     // ---------------- TMA producers: the deal, Q and K; V ----------------
     const bool kside = warp == C::kKWarp;
-    // cost of all own caches, then the request that this CTA's range of them starts in
-    long long own = 0;
-    for (int r = lane; kside && r < sh.R; r += 32) own += sh.own_total(sh.blocks_of(sh.ctx(r)));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
     const int cta = static_cast<int>(blockIdx.x);
-    const long long prefix_total = sh.prefix_total();
-    const Deal shared(sh, prefix_total, sh.prefix_cost), each(sh, own, sh.own_cost + kCostItem);
-    const long long pos = cta < each.n ? each.start(cta) : 0, end = cta < each.n ? each.start(cta + 1) : 0;
-    int r0 = 0;
-    long long at0 = 0;  // where request r0 starts
-    if (kside && end > pos) {
-      for (int base = 0; base < sh.R; base += 32) {
-        const long long c = base + lane < sh.R ? sh.own_total(sh.blocks_of(sh.ctx(base + lane))) : 0;
-        long long incl = c;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += up;
-        }
-        const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > pos);
-        if (over) {
-          const int src = __ffs(over) - 1;
-          r0 = base + src;
-          at0 += __shfl_sync(0xffffffffu, incl - c, src);
-          break;
-        }
-        at0 += __shfl_sync(0xffffffffu, incl, 31);
-      }
-    }
     const uint32_t stages = kside ? C::kKStages : C::kVStages;
     uint32_t g = 0, tile = 0;
     bool ok = true;
@@ -339,12 +381,8 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         ++i;
         if (s.kind >= 0) load(s);
       };
-      // the blocks of the item at `at`, of cost `all`, that start in [from, to)
-      auto cut = [&](long long from, long long to, long long at, long long all, int extra, int cost, int blocks, Segment& s) {
-        s.b0 = from <= at ? 0 : Deal::before(from, at, extra, cost, blocks);
-        s.n = (to >= at + all ? blocks : Deal::before(to, at, extra, cost, blocks)) - s.b0;
-        return s.n > 0;
-      };
+      const long long prefix_total = sh.prefix_total();
+      const Deal shared(prefix_total, sh.prefix_cost, sh.grid);
       if (cta < shared.n && prefix_total > 0) {
         const long long from = shared.start(cta), to = shared.start(cta + 1);
         const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
@@ -356,32 +394,14 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           s.r = 0;
           s.keys = sh.P;
           s.rec = k + cta;
-          if (cut(from, to, k * cost, cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
+          if (OwnWalk::cut(from, to, k * cost, cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
         }
       }
-      const int per_r = sh.Hkv * sh.own_items;
-      for (int r = r0; ok && r < sh.R && at0 < end; ++r) {
-        const int keys = sh.ctx(r), nb = sh.blocks_of(keys);
-        const long long cost = sh.own_item(nb);
-        if (nb > 0) {
-          int h = pos > at0 ? static_cast<int>((pos - at0) / cost) : 0;
-          Segment s;
-          s.head = h / sh.own_items;
-          s.item = h - s.head * sh.own_items;
-          s.r = r;
-          s.keys = keys;
-          for (long long at = at0 + h * cost; ok && h < per_r && at < end; ++h, at += cost) {
-            s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
-            s.rec = r * per_r + h + cta;
-            if (cut(pos, end, at, cost, kCostItem, sh.own_cost, nb, s)) publish(s);
-            if (++s.item == sh.own_items) {
-              s.item = 0;
-              ++s.head;
-            }
-          }
-        }
-        at0 += cost * per_r;
-      }
+      if (ok && !sh.small)
+        OwnWalk(sh, cta, lane).each_segment(sh, [&](const Segment& s) {
+          publish(s);
+          return ok;
+        });
       Segment last{};
       last.kind = -1;
       if (ok) publish(last);
@@ -650,6 +670,272 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
   if (warp == C::kMmaWarp) tmem_free_cols(tmem, 512);
 }
 
+// ---------------------------------------------------------------------------
+// Own caches with few rows per key head
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// the 16-byte piece with element (row, col) of rows of 64 elements that TMA wrote with the 128-byte swizzle
+__device__ __forceinline__ uint32_t swz(uint32_t box, int row, int col) {
+  return box + row * 128 + ((((col >> 3) ^ row) & 7) << 4);
+}
+
+// A CTA's ring holds blocks of 64 keys and, with a segment's first block, its q.
+// Four warps per 16 rows take 16 keys of a block each, with a maximum, a sum and an
+// output of their own, which they join over shared memory at the segment's end.
+template <int HD, int MT>
+struct Small {
+  static constexpr int kWarps = 4 * MT;
+  static constexpr int kThreads = 32 * (kWarps + 1);  // and a warp that walks the deal and loads
+  static constexpr int kKeys = 1 << kSmallShift;
+  static constexpr int kChunks = HD / 64;
+  static constexpr int kTileBytes = kKeys * HD * 2;     // K or V of a block
+  static constexpr int kOffQ = 2 * kTileBytes, kQChunk = 16 * MT * 128;
+  static constexpr int kStageBytes = kOffQ + kChunks * kQChunk;
+  static constexpr int kStages = 108 * 1024 * MT / kStageBytes;  // two CTAs per SM with 16 rows, one with 32
+  static constexpr int kOffBlocks = kStages * kStageBytes;       // what each stage holds
+  static constexpr int kOffBar = kOffBlocks + 32 * kStages;      // full and empty per stage, join, abort flag
+  static constexpr int kOffStats = kOffBar + 16 * kStages + 16;  // a maximum and a sum per warp and row
+  static constexpr int kSmemBytes = kOffStats + kWarps * 16 * 8;
+};
+struct OwnBlock {
+  int r, head, keys, key0, first, last, rec, pad;  // keys < 0 ends
+};
+
+template <int HD, int MT>
+__global__ void __launch_bounds__(Small<HD, MT>::kThreads, MT == 1 ? 2 : 1)
+own_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_log2, float2* __restrict__ rec_ml,
+                float* __restrict__ rec_o, int after_prefix) {
+  using C = Small<HD, MT>;
+  pdl_trigger();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t s0 = smem_u32(smem), bar0 = s0 + C::kOffBar;
+  if (s0 & 1023u) {  // the swizzled tiles need 1024-byte alignment
+    if (threadIdx.x == 0) atomicOr(&g_mtp_error_word, MTP_DEVERR_TIMEOUT);
+    return;
+  }
+  auto full = [&](uint32_t g) { return bar0 + 8u * (g % C::kStages); };
+  auto empty = [&](uint32_t g) { return bar0 + 8u * (C::kStages + g % C::kStages); };
+  const uint32_t join_bar = bar0 + 16u * C::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 16 * C::kStages + 8);
+  OwnBlock* blocks = reinterpret_cast<OwnBlock*>(smem + C::kOffBlocks);
+  float2* stats = reinterpret_cast<float2*>(smem + C::kOffStats);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), C::kWarps);
+    }
+    mbar_init(join_bar, C::kWarps);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  __syncthreads();
+  auto wwait = [&](uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, &g_mtp_error_word));
+  };
+  if (warp == C::kWarps) {
+    uint32_t g = 0;
+    auto stage_free = [&]() { return g < C::kStages || wwait(empty(g), (g / C::kStages - 1) & 1); };
+    const bool ok = OwnWalk(sh, blockIdx.x, lane).each_segment(sh, [&](const Segment& s) {
+      for (int j = 0; j < s.n; ++j, ++g) {
+        if (!stage_free()) return false;
+        const int key0 = (s.b0 + j) * C::kKeys, boxes = min((s.keys - key0 + kSmallBox - 1) / kSmallBox, C::kKeys / kSmallBox);
+        const uint32_t at = s0 + (g % C::kStages) * C::kStageBytes, bar = full(g);
+        if (lane == 0) {
+          blocks[g % C::kStages] = OwnBlock{s.r, s.head, s.keys, key0, j == 0, j + 1 == s.n, s.rec, 0};
+          mbar_expect_tx(bar, boxes * kSmallBox * HD * 4 + (j == 0 ? sh.own_rec * HD * 2 : 0));
+        }
+        __syncwarp();
+        constexpr int kPer = C::kKeys / kSmallBox * C::kChunks;  // boxes of K, of V
+        const int i = lane % kPer, c = i % C::kChunks, b = i / C::kChunks;
+        if (lane < 2 * kPer) {
+          if (b < boxes)
+            tma_tile_4d(at + (lane < kPer ? 0 : C::kTileBytes) + c * (C::kKeys * 128) + b * (kSmallBox * 128),
+                        lane < kPer ? &maps.kk : &maps.kv, 64 * c, s.head, key0 + b * kSmallBox, s.r, bar);
+        } else if (j == 0 && lane < 2 * kPer + C::kChunks) {
+          const int cq = lane - 2 * kPer;
+          tma_tile_4d(at + C::kOffQ + cq * C::kQChunk, &maps.q_own, 64 * cq, s.head * sh.G, 0, s.r, bar);
+        }
+      }
+      return true;
+    });
+    if (ok && stage_free()) {
+      if (lane == 0) {
+        blocks[g % C::kStages].keys = -1;
+        mbar_arrive1(full(g));
+      }
+      ++g;
+    }
+    // no copy may still be landing when the CTA leaves (matters only after an abort)
+    for (uint32_t x = g > C::kStages ? g - C::kStages : 0; x < g; ++x) wait_drain(full(x), (x / C::kStages) & 1, kWaitLimitCycles);
+  } else {
+    const int m = warp >> 2, part = warp & 3, gr = lane >> 2, t4 = lane & 3;  // rows 16 m .., keys 16 part ..
+    uint32_t syncs = 0;
+    auto join = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(join_bar);
+      return wwait(join_bar, syncs++ & 1);
+    };
+    int token[2];  // of rows gr and gr + 8
+    bool live[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rho = 16 * m + 8 * e + gr;
+      live[e] = rho < sh.own_rec;
+      token[e] = rho / sh.G;
+    }
+    uint32_t qa[HD / 16][4];
+    float mx[2], sum[2], o[HD / 8][4];
+    for (uint32_t g = 0;; ++g) {
+      if (!wwait(full(g), (g / C::kStages) & 1)) break;
+      const OwnBlock b = blocks[g % C::kStages];
+      if (b.keys < 0) break;
+      const uint32_t k_at = s0 + (g % C::kStages) * C::kStageBytes, v_at = k_at + C::kTileBytes;
+      if (b.first) {
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k)
+          ldsm_x4(swz(k_at + C::kOffQ + (k >> 2) * C::kQChunk, 16 * m + (lane & 15), 16 * (k & 3) + 8 * (lane >> 4)), qa[k]);
+        mx[0] = mx[1] = -INFINITY;
+        sum[0] = sum[1] = 0.f;
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      }
+      const int mine = b.keys - b.key0 - 16 * part;  // this warp's keys
+      if (mine > 0) {
+        if (mine < 16) {  // V rows past the end
+          uint8_t* v = smem + (v_at - s0) + (16 * part + mine) * 128;
+          for (int i = lane; i < (16 - mine) * 8 * C::kChunks; i += 32)
+            *reinterpret_cast<uint4*>(v + (i % C::kChunks) * (C::kKeys * 128) + i / C::kChunks * 16) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+        }
+        float sc[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {  // keys 0-7 and 8-15, 16 dimensions
+          uint32_t f[4];
+          ldsm_x4(swz(k_at + (k >> 2) * (C::kKeys * 128), 16 * part + (lane & 7) + 8 * (lane >> 4), 16 * (k & 3) + (lane & 8)), f);
+          mma_16816(sc[0], qa[k], f[0], f[1]);
+          mma_16816(sc[1], qa[k], f[2], f[3]);
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // keys of these 16 that the row sees
+          const int see = !live[e] ? 0 : sh.causal ? mine - sh.L + 1 + token[e] : mine;
+          float v[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = 8 * (i >> 1) + 2 * t4 + (i & 1) < see ? sc[i >> 1][2 * e + (i & 1)] : -INFINITY;
+          float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * scale_log2;
+          // a new running maximum only when the block's exceeds the stale one by 2^8
+          const float now = top > mx[e] + kStaleMaxLog2 ? top : mx[e];
+          const float neg = now == -INFINITY ? 0.f : -now;
+          const float alpha = now == mx[e] ? 1.f : ex2(mx[e] + neg);
+          mx[e] = now;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = ex2(fmaf(v[i], scale_log2, neg));
+          sum[e] = sum[e] * alpha + ((v[0] + v[1]) + (v[2] + v[3]));
+          pa[e] = pack2_bf16(v[0], v[1]);
+          pa[2 + e] = pack2_bf16(v[2], v[3]);
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int n = 0; n < HD / 8; ++n) {
+              o[n][2 * e] *= alpha;
+              o[n][2 * e + 1] *= alpha;
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < HD / 16; ++n) {
+          uint32_t f[4];
+          ldsm_x4_t(swz(v_at + (n >> 2) * (C::kKeys * 128), 16 * part + (lane & 15), 16 * (n & 3) + 8 * (lane >> 4)), f);
+          mma_16816(o[2 * n], pa, f[0], f[1]);
+          mma_16816(o[2 * n + 1], pa, f[2], f[3]);
+        }
+      }
+      if (b.last) {
+        float2* st = stats + m * 64;  // [part][row]
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
+          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
+          if (t4 == 0) st[part * 16 + 8 * e + gr] = make_float2(mx[e], sum[e]);
+        }
+        if (!join()) break;  // every warp is done with the stage: its K and V make room for the parts
+        const long long rec = sh.own_rec0 + static_cast<long long>(b.rec) * sh.own_rec;
+        float w[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float M = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) M = fmaxf(M, st[p * 16 + 8 * e + gr].x);
+          const float z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float2 a = st[p * 16 + 8 * e + gr];
+            l += ex2(a.x - z) * a.y;
+          }
+          w[e] = ex2(mx[e] - z);
+          if (part == 0 && t4 == 0 && live[e]) rec_ml[rec + 16 * m + 8 * e + gr] = make_float2(M, l);
+        }
+        // [m][part][row][HD / MT] in MT rounds, groups of 8 columns swizzled by the row
+        constexpr int kCols = HD / MT;
+        float* parts = reinterpret_cast<float*>(smem + (k_at - s0)) + m * 4 * 16 * kCols;
+        bool ok = true;
+#pragma unroll
+        for (int round = 0; round < MT; ++round) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int n = 0; n < kCols / 8; ++n)
+              *reinterpret_cast<float2*>(parts + (part * 16 + 8 * e + gr) * kCols + 8 * (n ^ (gr & (kCols / 8 - 1))) + 2 * t4) =
+                  make_float2(o[round * (kCols / 8) + n][2 * e] * w[e], o[round * (kCols / 8) + n][2 * e + 1] * w[e]);
+          if (!join()) { ok = false; break; }
+          for (int i = part * 32 + lane; i < 16 * (kCols / 4); i += 128) {
+            const int row = i / (kCols / 4), c = i % (kCols / 4);
+            if (16 * m + row >= sh.own_rec) break;
+            const float* src = parts + row * kCols + 8 * ((c >> 1) ^ (row & 7 & (kCols / 8 - 1))) + 4 * (c & 1);
+            float4 t = *reinterpret_cast<const float4*>(src);
+#pragma unroll
+            for (int p = 1; p < 4; ++p) {
+              const float4 a = *reinterpret_cast<const float4*>(src + p * 16 * kCols);
+              t.x += a.x;
+              t.y += a.y;
+              t.z += a.z;
+              t.w += a.w;
+            }
+            *reinterpret_cast<float4*>(rec_o + (rec + 16 * m + row) * HD + round * kCols + 4 * c) = t;
+          }
+          if (round + 1 < MT && !join()) { ok = false; break; }
+        }
+        if (!ok) break;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next copy overwrites what was written here
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(empty(g));
+    }
+  }
+  __syncthreads();
+  if (after_prefix) pdl_wait();  // complete only once the prefix kernel is, which it may run beside
+}
+
 // Joins the records of one (request, token, head) per warp: lanes over the
 // records for the maximum and the weights, then over the head's dimensions.
 template <int HD>
@@ -662,7 +948,7 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
   // cost of all requests' own caches, and of those before r
   long long sum = 0, before = 0;
   for (int i = threadIdx.x; i < sh.R; i += 256) {
-    const long long c = sh.own_total(sh.blocks_of(sh.ctx(i)));
+    const long long c = sh.own_total(sh.own_blocks(i));
     sum += c;
     if (i < r) before += c;
   }
@@ -686,7 +972,7 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
   const int item = blockIdx.x * 8 + warp;
   if (item >= sh.L * sh.H) return;
   const int i = item / sh.H, h = item - i * sh.H, head = h / sh.G, hg = h - head * sh.G;
-  const Deal shared(sh, sh.prefix_total(), sh.prefix_cost), each(sh, all, sh.own_cost + kCostItem);
+  const Deal shared(sh.prefix_total(), sh.prefix_cost, sh.grid), each(all, sh.own_cost + sh.own_extra, sh.own_ctas);
   // record rows: `n` segments from record row `at` on, `rows` apart, each with `halves` parts rows / 2 apart
   struct Run {
     long long at;
@@ -706,14 +992,16 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
     }
   }
   {
+    // the small-row kernel leaves one part per segment, the other two
     const bool two = (group | 1) < sh.groups;
-    const int nb = sh.blocks_of(sh.ctx(r)), k = head * sh.own_items + group / 2;
+    const int nb = sh.own_blocks(r), k = head * sh.own_items + group / 2, per = sh.small ? 1 : 2;
     const long long cost = sh.own_item(nb), at = prev + k * cost;
-    run[1] = Run{0, 0, 2 * sh.own_rec, two ? 1 : 2};
+    run[1] = Run{0, 0, per * sh.own_rec, two || sh.small ? 1 : 2};
     if (nb > 0) {
       const int a = each.owner(at), b = each.owner(nb > 1 ? at + cost - sh.own_cost : at);
       run[1].n = b - a + 1;
-      run[1].at = sh.own_rec0 + (2ll * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
+      run[1].at = sh.own_rec0 +
+                  (static_cast<long long>(per) * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
     }
   }
   const int n0 = run[0].n * run[0].halves, parts = n0 + run[1].n * run[1].halves;
@@ -809,15 +1097,22 @@ Shape make_shape(int R, int L, int H, int Hkv, int P, int T) {
   s.prefix_blocks = Shape::blocks_of(P);
   s.prefix_cost = s.prefix_tiles > 1 ? kCostTwo : kCostOne;
   s.own_items = (s.groups + 1) / 2;
-  s.own_cost = s.groups > 1 ? kCostTwo : kCostOne;
+  s.small = L * s.G <= kSmallRows ? (L * s.G + 15) / 16 : 0;
+  s.own_cost = s.small ? kSmallCost : s.groups > 1 ? kCostTwo : kCostOne;
+  s.own_extra = s.small ? kSmallCostItem : kCostItem;
+  s.own_shift = s.small ? kSmallShift : 7;
   s.own_rec = s.tokens * s.G;
   s.prefix_rec = s.requests * s.own_rec;
   s.grid = sm_count_current();
+  s.own_ctas = s.small == 1 ? 2 * s.grid : s.grid;
+  if (s.small)
+    s.own_ctas = static_cast<int>(std::min<long long>(s.own_ctas, static_cast<long long>(R) * Hkv * ((T + 63) / 64)));
   s.own_rec0 = P > 0 ? 2 * (static_cast<long long>(Hkv) * s.prefix_items + s.grid) * s.prefix_rec : 0;
   return s;
 }
 long long record_rows(const Shape& s) {
-  return s.own_rec0 + (s.T > 0 ? 2 * (static_cast<long long>(s.R) * s.Hkv * s.own_items + s.grid) * s.own_rec : 0);
+  const int per = s.small ? 1 : 2;
+  return s.own_rec0 + (s.T > 0 ? per * (static_cast<long long>(s.R) * s.Hkv * s.own_items + s.own_ctas) * s.own_rec : 0);
 }
 
 // rows as (dimension, head, token, request); boxes of 64 dimensions of heads x tokens x requests
@@ -828,6 +1123,21 @@ bool row_map(CUtensorMap* m, const void* p, int hd, int heads, int tokens, int r
   const uint64_t strides[3] = {static_cast<uint64_t>(s_h) * 2, static_cast<uint64_t>(s_t) * 2, static_cast<uint64_t>(s_r) * 2};
   const uint32_t boxes[4] = {64, static_cast<uint32_t>(box_h), static_cast<uint32_t>(box_t), static_cast<uint32_t>(box_r)};
   return tensor_map_bf16_4d(m, p, dims, strides, boxes);
+}
+
+template <int HD, int MT>
+mtp_status launch_own(const Shape& s, const Maps& m, float scale_log2, float2* ml, float* ro, bool after_prefix, cudaStream_t st) {
+  using C = Small<HD, MT>;
+  static PerDevice attr;
+  auto kernel = own_attn_kernel<HD, MT>;
+  if (!smem_limit(attr, kernel, C::kSmemBytes)) return MTP_ERR_CUDA;
+  if (after_prefix)
+    MTP_CUDA_TRY(launch_pdl(kernel, dim3(s.own_ctas), dim3(C::kThreads), C::kSmemBytes, st, m, s, scale_log2, ml, ro, 1));
+  else
+    kernel<<<s.own_ctas, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro, 0);
+  note_launch();
+  MTP_LAUNCH_CHECK();
+  return MTP_OK;
 }
 
 template <int HD>
@@ -841,16 +1151,24 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
        !row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1) ||
        !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
     return MTP_ERR_CUDA;
+  const int box = s.small ? kSmallBox : 64;
   if (p.T > 0 &&
       (!row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1) ||
-       !row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1) ||
-       !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, 64, 1)))
+       !row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, box, 1) ||
+       !row_map(&m.kv, p.kv, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, box, 1)))
     return MTP_ERR_CUDA;
   const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
-  if (p.P > 0 || p.T > 0) {
-    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(m, s, scale * kLog2e, ml, ro);
+  const float scale_log2 = scale * kLog2e;
+  const bool tiles = p.P > 0 || (p.T > 0 && !s.small);
+  if (tiles) {
+    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro);
     note_launch();
     MTP_LAUNCH_CHECK();
+  }
+  if (p.T > 0 && s.small) {
+    const mtp_status e =
+        s.small == 1 ? launch_own<HD, 1>(s, m, scale_log2, ml, ro, tiles, st) : launch_own<HD, 2>(s, m, scale_log2, ml, ro, tiles, st);
+    if (e != MTP_OK) return e;
   }
   const dim3 grid((s.L * s.H + 7) / 8, s.R);
   if (p.P > 0 || p.T > 0)
