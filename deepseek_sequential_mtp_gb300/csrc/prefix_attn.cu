@@ -58,10 +58,9 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 // costs for the deal: a block with one row tile, with two, and what a segment
 // of a request's own cache costs besides
 constexpr int kCostOne = 6, kCostTwo = 11, kCostItem = 5;
-// own caches of requests with up to kSmallRows rows per key head have a kernel of
-// their own, with blocks of 64 keys
-constexpr int kSmallBox = 32;  // ... brought in boxes of 32
-constexpr int kSmallRows = 32, kSmallShift = 6, kSmallCost = 2, kSmallCostItem = 1;
+// the small-row kernel: rows that it takes of a prefix, of an own cache; log2 of its
+// blocks' keys, keys of a box
+constexpr int kSmallPrefix = 16, kSmallOwn = 32, kSmallShift = 6, kSmallBox = 32, kSmallCost = 2, kSmallCostItem = 1;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -77,6 +76,8 @@ __device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__host__ __device__ constexpr int blocks_of(int keys, int shift) { return (keys + (1 << shift) - 1) >> shift; }
+
 // Sizes of the two kinds of items (over the prefix, over a request's own cache),
 // and where their records are.
 struct Shape {
@@ -85,21 +86,21 @@ struct Shape {
   int groups;        // token groups per request: ceil(L / tokens)
   int requests;      // requests per row tile of the prefix
   int prefix_tiles, prefix_items, prefix_blocks, prefix_cost;  // row tiles and items per key head; blocks; cost of one
+  int prefix_ctas;          // CTAs that share the prefix
   int own_items, own_cost, own_extra;  // row tiles of an own item: `groups` per key head; cost of a block, of an item besides
-  int own_shift, own_ctas;  // log2 of an own block's keys; CTAs that share the own caches
-  int small;                // row tiles of 16 of the small-row kernel, 0: own caches are the prefix kernel's too
+  int own_shift, own_ctas;  // log2 of a block's keys; CTAs that share the own caches
+  int prefix_small, own_small;  // tiles of 16 rows where the prefix, the own caches are the small-row kernel's, else 0
+  int prefix_per, own_per;  // parts that a segment leaves: 4 from the small-row kernel, else 2
   int prefix_rec, own_rec;  // record rows per row tile
   long long own_rec0;       // record row of the first own segment
-  int grid;
   const int32_t* ctx_len;
 
-  __host__ __device__ static int blocks_of(int len) { return (len + kKeys - 1) / kKeys; }
   __device__ __forceinline__ int ctx(int r) const { return ctx_len ? min(max(ctx_len[r], 0), T) : T; }
   __host__ __device__ long long prefix_total() const {
     return static_cast<long long>(Hkv) * prefix_items * prefix_blocks * prefix_cost;
   }
   // blocks of a request's own cache, cost of an item over them, and of all such items of the request
-  __device__ __forceinline__ int own_blocks(int r) const { return (ctx(r) + (1 << own_shift) - 1) >> own_shift; }
+  __device__ __forceinline__ int own_blocks(int r) const { return blocks_of(ctx(r), own_shift); }
   __device__ __forceinline__ long long own_item(int blocks) const {
     return blocks > 0 ? static_cast<long long>(blocks) * own_cost + own_extra : 0;
   }
@@ -141,20 +142,27 @@ struct Segment {
 };
 static_assert(sizeof(Segment) == 32, "two 16-byte words in the ring");
 
-// The part of the own caches' deal that CTA `cta` takes, walked by a warp.
-struct OwnWalk {
-  long long pos, end, at0;  // its range; where request r0, which the range starts in, starts
-  int r0, cta;
-  __device__ __forceinline__ OwnWalk(const Shape& sh, int cta_, int lane) : at0(0), r0(0), cta(cta_) {
-    long long own = 0;
-    for (int r = lane; r < sh.R; r += 32) own += sh.own_total(sh.own_blocks(r));
+// take(segment), by a whole warp, for each segment of CTA `cta`'s part of the prefix's
+// deal (if `prefix`), then of the own caches' (if `own`), until it returns false.
+template <typename Take>
+__device__ __forceinline__ bool each_segment(const Shape& sh, int cta, int lane, bool prefix, bool own, Take take) {
+#pragma unroll 1
+  for (int kind = prefix ? 0 : 1; kind < (own ? 2 : 1); ++kind) {
+    long long total = 0;
+    if (kind) {
+      for (int r = lane; r < sh.R; r += 32) total += sh.own_total(sh.own_blocks(r));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    const Deal each(own, sh.own_cost + sh.own_extra, sh.own_ctas);
-    pos = cta < each.n ? each.start(cta) : 0;
-    end = cta < each.n ? each.start(cta + 1) : 0;
-    if (end <= pos) return;
-    for (int base = 0; base < sh.R; base += 32) {
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    } else {
+      total = sh.prefix_total();
+    }
+    const int block = kind ? sh.own_cost : sh.prefix_cost, extra = kind ? sh.own_extra : 0;
+    const Deal deal(total, block + extra, kind ? sh.own_ctas : sh.prefix_ctas);
+    if (total <= 0 || cta >= deal.n) continue;
+    const long long from = deal.start(cta), to = deal.start(cta + 1);
+    int r = 0;  // request that the range starts in, and where it starts
+    long long start = 0;
+    for (int base = 0; kind && base < sh.R; base += 32) {
       const long long c = base + lane < sh.R ? sh.own_total(sh.own_blocks(base + lane)) : 0;
       long long incl = c;
 #pragma unroll
@@ -162,53 +170,43 @@ struct OwnWalk {
         const long long up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
-      const unsigned over = __ballot_sync(0xffffffffu, at0 + incl > pos);
+      const unsigned over = __ballot_sync(0xffffffffu, start + incl > from);
       if (over) {
         const int src = __ffs(over) - 1;
-        r0 = base + src;
-        at0 += __shfl_sync(0xffffffffu, incl - c, src);
-        return;
+        r = base + src;
+        start += __shfl_sync(0xffffffffu, incl - c, src);
+        break;
       }
-      at0 += __shfl_sync(0xffffffffu, incl, 31);
+      start += __shfl_sync(0xffffffffu, incl, 31);
     }
-  }
-  // take(segment) for each segment, until it returns false
-  template <typename Take>
-  __device__ __forceinline__ bool each_segment(const Shape& sh, Take take) const {
-    const int per_r = sh.Hkv * sh.own_items;
-    long long start = at0;
-    for (int r = r0; r < sh.R && start < end; ++r) {
-      const int keys = sh.ctx(r), nb = sh.own_blocks(r);
-      const long long cost = sh.own_item(nb);
-      if (nb > 0) {
-        int h = pos > start ? static_cast<int>((pos - start) / cost) : 0;
-        Segment s;
-        s.head = h / sh.own_items;
-        s.item = h - s.head * sh.own_items;
-        s.r = r;
-        s.keys = keys;
-        for (long long at = start + h * cost; h < per_r && at < end; ++h, at += cost) {
-          s.kind = 1 | (2 * s.item + 1 < sh.groups ? 2 : 0);
-          s.rec = r * per_r + h + cta;
-          if (cut(pos, end, at, cost, sh.own_extra, sh.own_cost, nb, s) && !take(s)) return false;
-          if (++s.item == sh.own_items) {
-            s.item = 0;
-            ++s.head;
-          }
+    const int items = kind ? sh.own_items : sh.prefix_items, tiles = kind ? sh.groups : sh.prefix_tiles, per_r = sh.Hkv * items;
+    for (; r < (kind ? sh.R : 1) && start < to; ++r) {
+      const int keys = kind ? sh.ctx(r) : sh.P, nb = kind ? sh.own_blocks(r) : sh.prefix_blocks;
+      if (nb == 0) continue;
+      const long long cost = static_cast<long long>(nb) * block + extra;
+      int k = from > start ? static_cast<int>((from - start) / cost) : 0;
+      Segment s;
+      s.head = k / items;
+      s.item = k - s.head * items;
+      s.r = r;
+      s.keys = keys;
+      for (long long at = start + k * cost; k < per_r && at < to; ++k, at += cost) {
+        // the item's blocks that start in [from, to)
+        s.b0 = from <= at ? 0 : Deal::before(from, at, extra, block, nb);
+        s.n = (to >= at + cost ? nb : Deal::before(to, at, extra, block, nb)) - s.b0;
+        s.kind = kind | (2 * s.item + 1 < tiles ? 2 : 0);
+        s.rec = r * per_r + k + cta;
+        if (s.n > 0 && !take(s)) return false;
+        if (++s.item == items) {
+          s.item = 0;
+          ++s.head;
         }
       }
       start += cost * per_r;
     }
-    return true;
   }
-  // the blocks of the item at `at`, of cost `all`, that start in [from, to)
-  static __device__ __forceinline__ bool cut(long long from, long long to, long long at, long long all, int extra, int cost,
-                                             int blocks, Segment& s) {
-    s.b0 = from <= at ? 0 : Deal::before(from, at, extra, cost, blocks);
-    s.n = (to >= at + all ? blocks : Deal::before(to, at, extra, cost, blocks)) - s.b0;
-    return s.n > 0;
-  }
-};
+  return true;
+}
 
 template <int HD>
 struct Cfg {
@@ -330,7 +328,6 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
   if (warp == C::kKWarp || warp == C::kVWarp) {
     // ---------------- TMA producers: the deal, Q and K; V ----------------
     const bool kside = warp == C::kKWarp;
-    const int cta = static_cast<int>(blockIdx.x);
     const uint32_t stages = kside ? C::kKStages : C::kVStages;
     uint32_t g = 0, tile = 0;
     bool ok = true;
@@ -381,27 +378,12 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         ++i;
         if (s.kind >= 0) load(s);
       };
-      const long long prefix_total = sh.prefix_total();
-      const Deal shared(prefix_total, sh.prefix_cost, sh.grid);
-      if (cta < shared.n && prefix_total > 0) {
-        const long long from = shared.start(cta), to = shared.start(cta + 1);
-        const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost;
-        for (int k = static_cast<int>(from / cost); ok && k < sh.Hkv * sh.prefix_items && k * cost < to; ++k) {
-          Segment s;
-          s.head = k / sh.prefix_items;
-          s.item = k - s.head * sh.prefix_items;
-          s.kind = 2 * s.item + 1 < sh.prefix_tiles ? 2 : 0;
-          s.r = 0;
-          s.keys = sh.P;
-          s.rec = k + cta;
-          if (OwnWalk::cut(from, to, k * cost, cost, 0, sh.prefix_cost, sh.prefix_blocks, s)) publish(s);
-        }
-      }
-      if (ok && !sh.small)
-        OwnWalk(sh, cta, lane).each_segment(sh, [&](const Segment& s) {
-          publish(s);
-          return ok;
-        });
+      const int cta = static_cast<int>(blockIdx.x);
+      auto take = [&](const Segment& s) {
+        publish(s);
+        return ok;
+      };
+      each_segment(sh, cta, lane, !sh.prefix_small, !sh.own_small, take);
       Segment last{};
       last.kind = -1;
       if (ok) publish(last);
@@ -695,32 +677,87 @@ __device__ __forceinline__ uint32_t swz(uint32_t box, int row, int col) {
   return box + row * 128 + ((((col >> 3) ^ row) & 7) << 4);
 }
 
-// A CTA's ring holds blocks of 64 keys and, with a segment's first block, its q.
-// Four warps per 16 rows take 16 keys of a block each, with a maximum, a sum and an
-// output of their own, which they join over shared memory at the segment's end.
+// A CTA's ring holds blocks of keys and, with a segment's first block, its q.  Four
+// warps have 16 rows, each 16 keys of a block, with a maximum, a sum and an output of
+// its own: four parts per segment.  (Joined over shared memory first, they cost 2400
+// cycles a segment, two waits for one another, against 300.)
 template <int HD, int MT>
 struct Small {
   static constexpr int kWarps = 4 * MT;
-  static constexpr int kThreads = 32 * (kWarps + 1);  // and a warp that walks the deal and loads
-  static constexpr int kKeys = 1 << kSmallShift;
-  static constexpr int kChunks = HD / 64;
-  static constexpr int kTileBytes = kKeys * HD * 2;     // K or V of a block
+  static constexpr int kThreads = 32 * (kWarps + 1);  // and a warp that walks the deals and loads
+  static constexpr int kCtas = 2 / MT;                // per SM
+  static constexpr int kBlock = 1 << kSmallShift;
+  static constexpr int kChunks = HD / 64, kChunkBytes = kBlock * 128;
+  static constexpr int kTileBytes = kBlock * HD * 2;  // K or V of a block
   static constexpr int kOffQ = 2 * kTileBytes, kQChunk = 16 * MT * 128;
   static constexpr int kStageBytes = kOffQ + kChunks * kQChunk;
-  static constexpr int kStages = 108 * 1024 * MT / kStageBytes;  // two CTAs per SM with 16 rows, one with 32
+  static constexpr int kStages = 108 * 1024 * MT / kStageBytes;
   static constexpr int kOffBlocks = kStages * kStageBytes;       // what each stage holds
-  static constexpr int kOffBar = kOffBlocks + 32 * kStages;      // full and empty per stage, join, abort flag
-  static constexpr int kOffStats = kOffBar + 16 * kStages + 16;  // a maximum and a sum per warp and row
-  static constexpr int kSmemBytes = kOffStats + kWarps * 16 * 8;
+  static constexpr int kOffBar = kOffBlocks + 16 * kStages;      // full and empty per stage, abort flag
+  static constexpr int kSmemBytes = kOffBar + 16 * kStages + 16;
 };
-struct OwnBlock {
-  int r, head, keys, key0, first, last, rec, pad;  // keys < 0 ends
+// 16 rows of a warp
+template <int HD>
+struct SmallRows {
+  uint32_t qa[HD / 16][4];
+  float mx[2], sum[2], o[HD / 8][4];
+  int hidden[2];  // keys at the item's end that rows g and g + 8 do not see
 };
+// ... and 16 keys of a block, `key` on, the item's last `left`
+template <int HD>
+__device__ __forceinline__ void small_block(SmallRows<HD>& w, uint32_t k_at, uint32_t v_at, int key, int left, float scale_log2, int lane) {
+  constexpr int kChunk = Small<HD, 1>::kChunkBytes;
+  const int t4 = lane & 3;
+  float sc[2][4] = {};
+#pragma unroll
+  for (int k = 0; k < HD / 16; ++k) {  // keys 0-7 and 8-15, 16 dimensions
+    uint32_t f[4];
+    ldsm_x4(swz(k_at + (k >> 2) * kChunk, key + (lane & 7) + 8 * (lane >> 4), 16 * (k & 3) + (lane & 8)), f);
+    mma_16816(sc[0], w.qa[k], f[0], f[1]);
+    mma_16816(sc[1], w.qa[k], f[2], f[3]);
+  }
+  uint32_t pa[4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int see = left - w.hidden[e];  // of these keys
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = 8 * (i >> 1) + 2 * t4 + (i & 1) < see ? sc[i >> 1][2 * e + (i & 1)] : -INFINITY;
+    float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * scale_log2;
+    // a new running maximum only when the block's exceeds the stale one by 2^8
+    const float now = top > w.mx[e] + kStaleMaxLog2 ? top : w.mx[e];
+    const float neg = now == -INFINITY ? 0.f : -now;
+    const float alpha = now == w.mx[e] ? 1.f : ex2(w.mx[e] + neg);
+    w.mx[e] = now;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ex2(fmaf(v[i], scale_log2, neg));
+    w.sum[e] = w.sum[e] * alpha + ((v[0] + v[1]) + (v[2] + v[3]));
+    pa[e] = pack2_bf16(v[0], v[1]);
+    pa[2 + e] = pack2_bf16(v[2], v[3]);
+    if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < HD / 8; ++n) {
+        w.o[n][2 * e] *= alpha;
+        w.o[n][2 * e + 1] *= alpha;
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < HD / 16; ++n) {
+    uint32_t f[4];
+    ldsm_x4_t(swz(v_at + (n >> 2) * kChunk, key + (lane & 15), 16 * (n & 3) + 8 * (lane >> 4)), f);
+    mma_16816(w.o[2 * n], pa, f[0], f[1]);
+    mma_16816(w.o[2 * n + 1], pa, f[2], f[3]);
+  }
+}
+enum : int { kFirst = 1, kLast = 2, kOwn = 4 };
 
 template <int HD, int MT>
-__global__ void __launch_bounds__(Small<HD, MT>::kThreads, MT == 1 ? 2 : 1)
-own_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_log2, float2* __restrict__ rec_ml,
-                float* __restrict__ rec_o, int after_prefix) {
+__global__ void __launch_bounds__(Small<HD, MT>::kThreads, Small<HD, MT>::kCtas)
+small_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_log2, float2* __restrict__ rec_ml,
+                  float* __restrict__ rec_o, int after) {
   using C = Small<HD, MT>;
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -731,17 +768,14 @@ own_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_l
   }
   auto full = [&](uint32_t g) { return bar0 + 8u * (g % C::kStages); };
   auto empty = [&](uint32_t g) { return bar0 + 8u * (C::kStages + g % C::kStages); };
-  const uint32_t join_bar = bar0 + 16u * C::kStages;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 16 * C::kStages + 8);
-  OwnBlock* blocks = reinterpret_cast<OwnBlock*>(smem + C::kOffBlocks);
-  float2* stats = reinterpret_cast<float2*>(smem + C::kOffStats);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffBar + 16 * C::kStages);
+  int4* blocks = reinterpret_cast<int4*>(smem + C::kOffBlocks);  // keys of the item (< 0 ends), first key, flags, record
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full(i), 1);
       mbar_init(empty(i), C::kWarps);
     }
-    mbar_init(join_bar, C::kWarps);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -753,32 +787,37 @@ own_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_l
   if (warp == C::kWarps) {
     uint32_t g = 0;
     auto stage_free = [&]() { return g < C::kStages || wwait(empty(g), (g / C::kStages - 1) & 1); };
-    const bool ok = OwnWalk(sh, blockIdx.x, lane).each_segment(sh, [&](const Segment& s) {
+    auto take = [&](const Segment& s) {
+      const bool own = s.kind & 1;
       for (int j = 0; j < s.n; ++j, ++g) {
         if (!stage_free()) return false;
-        const int key0 = (s.b0 + j) * C::kKeys, boxes = min((s.keys - key0 + kSmallBox - 1) / kSmallBox, C::kKeys / kSmallBox);
+        const int key0 = (s.b0 + j) * C::kBlock, boxes = min((s.keys - key0 + kSmallBox - 1) / kSmallBox, C::kBlock / kSmallBox);
         const uint32_t at = s0 + (g % C::kStages) * C::kStageBytes, bar = full(g);
         if (lane == 0) {
-          blocks[g % C::kStages] = OwnBlock{s.r, s.head, s.keys, key0, j == 0, j + 1 == s.n, s.rec, 0};
-          mbar_expect_tx(bar, boxes * kSmallBox * HD * 4 + (j == 0 ? sh.own_rec * HD * 2 : 0));
+          blocks[g % C::kStages] =
+              make_int4(s.keys, key0, (j == 0 ? kFirst : 0) | (j + 1 == s.n ? kLast : 0) | (own ? kOwn : 0), s.rec);
+          mbar_expect_tx(bar, boxes * kSmallBox * HD * 4 + (j == 0 ? (own ? sh.own_rec : sh.prefix_rec) * HD * 2 : 0));
         }
         __syncwarp();
-        constexpr int kPer = C::kKeys / kSmallBox * C::kChunks;  // boxes of K, of V
+        constexpr int kPer = C::kBlock / kSmallBox * C::kChunks;  // boxes of K, of V
         const int i = lane % kPer, c = i % C::kChunks, b = i / C::kChunks;
         if (lane < 2 * kPer) {
+          const bool k = lane < kPer;
           if (b < boxes)
-            tma_tile_4d(at + (lane < kPer ? 0 : C::kTileBytes) + c * (C::kKeys * 128) + b * (kSmallBox * 128),
-                        lane < kPer ? &maps.kk : &maps.kv, 64 * c, s.head, key0 + b * kSmallBox, s.r, bar);
+            tma_tile_4d(at + (k ? 0 : C::kTileBytes) + c * C::kChunkBytes + b * (kSmallBox * 128),
+                        own ? (k ? &maps.kk : &maps.kv) : (k ? &maps.pk : &maps.pv), 64 * c, s.head, key0 + b * kSmallBox, s.r, bar);
         } else if (j == 0 && lane < 2 * kPer + C::kChunks) {
           const int cq = lane - 2 * kPer;
-          tma_tile_4d(at + C::kOffQ + cq * C::kQChunk, &maps.q_own, 64 * cq, s.head * sh.G, 0, s.r, bar);
+          tma_tile_4d(at + C::kOffQ + cq * C::kQChunk, own ? &maps.q_own : &maps.q_prefix, 64 * cq, s.head * sh.G, 0, s.r, bar);
         }
       }
       return true;
-    });
+    };
+    const int cta = static_cast<int>(blockIdx.x);
+    const bool ok = each_segment(sh, cta, lane, sh.prefix_small, sh.own_small, take);
     if (ok && stage_free()) {
       if (lane == 0) {
-        blocks[g % C::kStages].keys = -1;
+        blocks[g % C::kStages] = make_int4(-1, 0, 0, 0);
         mbar_arrive1(full(g));
       }
       ++g;
@@ -786,256 +825,138 @@ own_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale_l
     // no copy may still be landing when the CTA leaves (matters only after an abort)
     for (uint32_t x = g > C::kStages ? g - C::kStages : 0; x < g; ++x) wait_drain(full(x), (x / C::kStages) & 1, kWaitLimitCycles);
   } else {
-    const int m = warp >> 2, part = warp & 3, gr = lane >> 2, t4 = lane & 3;  // rows 16 m .., keys 16 part ..
-    uint32_t syncs = 0;
-    auto join = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(join_bar);
-      return wwait(join_bar, syncs++ & 1);
-    };
-    int token[2];  // of rows gr and gr + 8
-    bool live[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rho = 16 * m + 8 * e + gr;
-      live[e] = rho < sh.own_rec;
-      token[e] = rho / sh.G;
-    }
-    uint32_t qa[HD / 16][4];
-    float mx[2], sum[2], o[HD / 8][4];
+    const int gr = lane >> 2, t4 = lane & 3;
+    const int first = warp & 4, row0 = 4 * first;  // the first of the four warps, their first row
+    const int key = 16 * (warp - first);           // a block's first key for this warp
+    SmallRows<HD> w;
     for (uint32_t g = 0;; ++g) {
       if (!wwait(full(g), (g / C::kStages) & 1)) break;
-      const OwnBlock b = blocks[g % C::kStages];
-      if (b.keys < 0) break;
+      const int4 b = blocks[g % C::kStages];
+      if (b.x < 0) break;
       const uint32_t k_at = s0 + (g % C::kStages) * C::kStageBytes, v_at = k_at + C::kTileBytes;
-      if (b.first) {
+      const bool own = b.z & kOwn;
+      const int rows = own ? sh.own_rec : sh.prefix_rec;
+      if (b.z & kFirst) {
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k)
-          ldsm_x4(swz(k_at + C::kOffQ + (k >> 2) * C::kQChunk, 16 * m + (lane & 15), 16 * (k & 3) + 8 * (lane >> 4)), qa[k]);
-        mx[0] = mx[1] = -INFINITY;
-        sum[0] = sum[1] = 0.f;
+          ldsm_x4(swz(k_at + C::kOffQ + (k >> 2) * C::kQChunk, row0 + (lane & 15), 16 * (k & 3) + 8 * (lane >> 4)), w.qa[k]);
 #pragma unroll
-        for (int n = 0; n < HD / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          w.mx[e] = -INFINITY;
+          w.sum[e] = 0.f;
+          const int row = row0 + 8 * e + gr;
+          w.hidden[e] = row >= rows ? 0x40000000 : own && sh.causal ? sh.L - 1 - row / sh.G : 0;
+        }
+#pragma unroll
+        for (int n = 0; n < HD / 8; ++n) w.o[n][0] = w.o[n][1] = w.o[n][2] = w.o[n][3] = 0.f;
       }
-      const int mine = b.keys - b.key0 - 16 * part;  // this warp's keys
-      if (mine > 0) {
-        if (mine < 16) {  // V rows past the end
-          uint8_t* v = smem + (v_at - s0) + (16 * part + mine) * 128;
-          for (int i = lane; i < (16 - mine) * 8 * C::kChunks; i += 32)
-            *reinterpret_cast<uint4*>(v + (i % C::kChunks) * (C::kKeys * 128) + i / C::kChunks * 16) = make_uint4(0, 0, 0, 0);
+      const int left = b.x - b.y - key;  // the item's keys from this warp's first on
+      if (left > 0) {
+        if (left < 16) {  // V rows past the end, by each warp that reads them (the same zeros)
+          uint8_t* v = smem + (v_at - s0) + (key + left) * 128;
+          for (int i = lane; i < (16 - left) * 8 * C::kChunks; i += 32)
+            *reinterpret_cast<uint4*>(v + (i % C::kChunks) * C::kChunkBytes + i / C::kChunks * 16) = make_uint4(0, 0, 0, 0);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later copy overwrites them
           __syncwarp();
         }
-        float sc[2][4] = {};
-#pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {  // keys 0-7 and 8-15, 16 dimensions
-          uint32_t f[4];
-          ldsm_x4(swz(k_at + (k >> 2) * (C::kKeys * 128), 16 * part + (lane & 7) + 8 * (lane >> 4), 16 * (k & 3) + (lane & 8)), f);
-          mma_16816(sc[0], qa[k], f[0], f[1]);
-          mma_16816(sc[1], qa[k], f[2], f[3]);
-        }
-        uint32_t pa[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // keys of these 16 that the row sees
-          const int see = !live[e] ? 0 : sh.causal ? mine - sh.L + 1 + token[e] : mine;
-          float v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = 8 * (i >> 1) + 2 * t4 + (i & 1) < see ? sc[i >> 1][2 * e + (i & 1)] : -INFINITY;
-          float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * scale_log2;
-          // a new running maximum only when the block's exceeds the stale one by 2^8
-          const float now = top > mx[e] + kStaleMaxLog2 ? top : mx[e];
-          const float neg = now == -INFINITY ? 0.f : -now;
-          const float alpha = now == mx[e] ? 1.f : ex2(mx[e] + neg);
-          mx[e] = now;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = ex2(fmaf(v[i], scale_log2, neg));
-          sum[e] = sum[e] * alpha + ((v[0] + v[1]) + (v[2] + v[3]));
-          pa[e] = pack2_bf16(v[0], v[1]);
-          pa[2 + e] = pack2_bf16(v[2], v[3]);
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-            for (int n = 0; n < HD / 8; ++n) {
-              o[n][2 * e] *= alpha;
-              o[n][2 * e + 1] *= alpha;
-            }
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < HD / 16; ++n) {
-          uint32_t f[4];
-          ldsm_x4_t(swz(v_at + (n >> 2) * (C::kKeys * 128), 16 * part + (lane & 15), 16 * (n & 3) + 8 * (lane >> 4)), f);
-          mma_16816(o[2 * n], pa, f[0], f[1]);
-          mma_16816(o[2 * n + 1], pa, f[2], f[3]);
-        }
+        small_block<HD>(w, k_at, v_at, key, left, scale_log2, lane);
       }
-      if (b.last) {
-        float2* st = stats + m * 64;  // [part][row]
+      if (b.z & kLast) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 1);
-          sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], 2);
-          if (t4 == 0) st[part * 16 + 8 * e + gr] = make_float2(mx[e], sum[e]);
+          w.sum[e] += __shfl_xor_sync(0xffffffffu, w.sum[e], 1);
+          w.sum[e] += __shfl_xor_sync(0xffffffffu, w.sum[e], 2);
         }
-        if (!join()) break;  // every warp is done with the stage: its K and V make room for the parts
-        const long long rec = sh.own_rec0 + static_cast<long long>(b.rec) * sh.own_rec;
-        float w[2];
+        // a part of the segment's records per warp with the same rows
+        const long long rec = (own ? sh.own_rec0 : 0) + (4ll * b.w + (warp & 3)) * rows + row0;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float M = -INFINITY, l = 0.f;
+          const int row = 8 * e + gr;
+          if (row0 + row < rows) {
+            if (t4 == 0) rec_ml[rec + row] = make_float2(w.mx[e], w.sum[e]);
+            if (w.sum[e] != 0.f) {  // a part without a key is not read
+              float* to = rec_o + (rec + row) * HD + 2 * t4;
 #pragma unroll
-          for (int p = 0; p < 4; ++p) M = fmaxf(M, st[p * 16 + 8 * e + gr].x);
-          const float z = M == -INFINITY ? 0.f : M;
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const float2 a = st[p * 16 + 8 * e + gr];
-            l += ex2(a.x - z) * a.y;
-          }
-          w[e] = ex2(mx[e] - z);
-          if (part == 0 && t4 == 0 && live[e]) rec_ml[rec + 16 * m + 8 * e + gr] = make_float2(M, l);
-        }
-        // [m][part][row][HD / MT] in MT rounds, groups of 8 columns swizzled by the row
-        constexpr int kCols = HD / MT;
-        float* parts = reinterpret_cast<float*>(smem + (k_at - s0)) + m * 4 * 16 * kCols;
-        bool ok = true;
-#pragma unroll
-        for (int round = 0; round < MT; ++round) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int n = 0; n < kCols / 8; ++n)
-              *reinterpret_cast<float2*>(parts + (part * 16 + 8 * e + gr) * kCols + 8 * (n ^ (gr & (kCols / 8 - 1))) + 2 * t4) =
-                  make_float2(o[round * (kCols / 8) + n][2 * e] * w[e], o[round * (kCols / 8) + n][2 * e + 1] * w[e]);
-          if (!join()) { ok = false; break; }
-          for (int i = part * 32 + lane; i < 16 * (kCols / 4); i += 128) {
-            const int row = i / (kCols / 4), c = i % (kCols / 4);
-            if (16 * m + row >= sh.own_rec) break;
-            const float* src = parts + row * kCols + 8 * ((c >> 1) ^ (row & 7 & (kCols / 8 - 1))) + 4 * (c & 1);
-            float4 t = *reinterpret_cast<const float4*>(src);
-#pragma unroll
-            for (int p = 1; p < 4; ++p) {
-              const float4 a = *reinterpret_cast<const float4*>(src + p * 16 * kCols);
-              t.x += a.x;
-              t.y += a.y;
-              t.z += a.z;
-              t.w += a.w;
+              for (int n = 0; n < HD / 8; ++n) *reinterpret_cast<float2*>(to + 8 * n) = make_float2(w.o[n][2 * e], w.o[n][2 * e + 1]);
             }
-            *reinterpret_cast<float4*>(rec_o + (rec + 16 * m + row) * HD + round * kCols + 4 * c) = t;
           }
-          if (round + 1 < MT && !join()) { ok = false; break; }
         }
-        if (!ok) break;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the next copy overwrites what was written here
       }
       __syncwarp();
       if (lane == 0) mbar_arrive1(empty(g));
     }
   }
   __syncthreads();
-  if (after_prefix) pdl_wait();  // complete only once the prefix kernel is, which it may run beside
+  if (after) pdl_wait();  // complete only once the kernel before is, which it may run beside
 }
 
-// Joins the records of one (request, token, head) per warp: lanes over the
-// records for the maximum and the weights, then over the head's dimensions.
+// Joins the records of one (request, token, head) per warp: a lane per record for the
+// maxima and the weights, then lanes over the head's dimensions.  The deals come from
+// ctx_len alone, so all of that runs under the kernels before; what is left then is one
+// chain of loads, in which the first records' outputs are asked for with their maxima.
+constexpr int kJoinWarps = 4;
 template <int HD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const float* __restrict__ rec_o,
                    __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
-  __shared__ long long s_sum[8], s_before[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y;
-  // cost of all requests' own caches, and of those before r
-  long long sum = 0, before = 0;
-  for (int i = threadIdx.x; i < sh.R; i += 256) {
-    const long long c = sh.own_total(sh.own_blocks(i));
-    sum += c;
-    if (i < r) before += c;
+  const int r = blockIdx.y, item = blockIdx.x * kJoinWarps + warp;
+  if (item >= sh.L * sh.H) {
+    pdl_wait();
+    return;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  if (lane == 0) {
-    s_sum[warp] = sum;
-    s_before[warp] = before;
-  }
-  __syncthreads();
-  long long all = 0, prev = 0;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) {
-    all += s_sum[w];
-    prev += s_before[w];
-  }
-  pdl_wait();  // the records are the previous kernel's
-  const int item = blockIdx.x * 8 + warp;
-  if (item >= sh.L * sh.H) return;
   const int i = item / sh.H, h = item - i * sh.H, head = h / sh.G, hg = h - head * sh.G;
-  const Deal shared(sh.prefix_total(), sh.prefix_cost, sh.grid), each(all, sh.own_cost + sh.own_extra, sh.own_ctas);
-  // record rows: `n` segments from record row `at` on, `rows` apart, each with `halves` parts rows / 2 apart
-  struct Run {
-    long long at;
-    int n, rows, halves;
-  } run[2];
   const int group = i / sh.tokens, in = (i - group * sh.tokens) * sh.G + hg;  // row of a tile that starts at the request
-  {
+  // parts of a kind: `per` a segment from record row `at` on, `step` rows apart
+  long long at0 = 0, at1 = 0;
+  int n0 = 0, n1 = 0, step0 = 0, step1 = 0;
+  if (sh.prefix_blocks > 0) {
+    const Deal shared(sh.prefix_total(), sh.prefix_cost, sh.prefix_ctas);
     const int tile = r / sh.requests * sh.groups + group, row = r % sh.requests * sh.tokens * sh.G + in;
     const bool two = (tile | 1) < sh.prefix_tiles;
     const int k = head * sh.prefix_items + tile / 2;
     const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost, at = k * cost;
-    run[0] = Run{0, 0, 2 * sh.prefix_rec, two ? 1 : 2};
-    if (cost > 0) {
-      const int a = shared.owner(at), b = shared.owner(at + cost - sh.prefix_cost);
-      run[0].n = b - a + 1;
-      run[0].at = (2ll * (k + a) + (two ? tile & 1 : 0)) * sh.prefix_rec + row;
-    }
+    const int a = shared.owner(at), b = shared.owner(at + cost - sh.prefix_cost);
+    // two row tiles leave a part each and this row has every other one, else they are all this row's
+    n0 = (b - a + 1) * (two ? 1 : sh.prefix_per);
+    step0 = (two ? 2 : 1) * sh.prefix_rec;
+    at0 = (static_cast<long long>(sh.prefix_per) * (k + a) + (two ? tile & 1 : 0)) * sh.prefix_rec + row;
   }
-  {
-    // the small-row kernel leaves one part per segment, the other two
+  const int nb = sh.own_blocks(r);
+  if (nb > 0) {
+    // cost of all requests' own caches, and of those before r
+    long long all = 0, prev = 0;
+    for (int q = lane; q < sh.R; q += 32) {
+      const long long c = sh.own_total(sh.own_blocks(q));
+      all += c;
+      if (q < r) prev += c;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      all += __shfl_xor_sync(0xffffffffu, all, d);
+      prev += __shfl_xor_sync(0xffffffffu, prev, d);
+    }
+    const Deal each(all, sh.own_cost + sh.own_extra, sh.own_ctas);
     const bool two = (group | 1) < sh.groups;
-    const int nb = sh.own_blocks(r), k = head * sh.own_items + group / 2, per = sh.small ? 1 : 2;
+    const int k = head * sh.own_items + group / 2;
     const long long cost = sh.own_item(nb), at = prev + k * cost;
-    run[1] = Run{0, 0, per * sh.own_rec, two || sh.small ? 1 : 2};
-    if (nb > 0) {
-      const int a = each.owner(at), b = each.owner(nb > 1 ? at + cost - sh.own_cost : at);
-      run[1].n = b - a + 1;
-      run[1].at = sh.own_rec0 +
-                  (static_cast<long long>(per) * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
-    }
+    const int a = each.owner(at), b = each.owner(nb > 1 ? at + cost - sh.own_cost : at);
+    n1 = (b - a + 1) * (two ? 1 : sh.own_per);
+    step1 = (two ? 2 : 1) * sh.own_rec;
+    at1 = sh.own_rec0 +
+          (static_cast<long long>(sh.own_per) * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
   }
-  const int n0 = run[0].n * run[0].halves, parts = n0 + run[1].n * run[1].halves;
-  auto part_at = [&](int p) {
-    const Run& u = run[p < n0 ? 0 : 1];
-    const int e = p < n0 ? p : p - n0, seg = e / u.halves, half = e - seg * u.halves;
-    return u.at + static_cast<long long>(seg) * u.rows + half * (u.rows / 2);
-  };
-  float M = -INFINITY;
-  for (int p = lane; p < parts; p += 32) {
-    const float2 ml = rec_ml[part_at(p)];
-    if (ml.y > 0.f || ml.y != ml.y) M = fmaxf(M, ml.x);
-  }
-  M = warp_max(M);
-  const float Ms = M == -INFINITY ? 0.f : M;
+  const int parts = n0 + n1;
   constexpr int kD = HD / 32;
-  float acc[kD], L = 0.f;
+  float acc[kD], L = 0.f, M = -INFINITY;  // L: this lane's records
 #pragma unroll
   for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+  pdl_wait();  // the records are earlier kernels'
   for (int p0 = 0; p0 < parts; p0 += 32) {
-    long long at = 0;
-    float w = 0.f;
-    if (p0 + lane < parts) {
-      at = part_at(p0 + lane);
-      const float2 ml = rec_ml[at];
-      if (ml.y > 0.f || ml.y != ml.y) {
-        w = ex2(ml.x - Ms);
-        L += w * ml.y;
-      }
-    }
-    const int n = min(32, parts - p0);
-    // eight parts' outputs in flight; a part without a key has left none
-    for (int e0 = 0; e0 < n; e0 += 8) {
-      float v[8][kD];
+    const int p = min(p0 + lane, parts - 1), n = min(32, parts - p0);
+    const long long at = p < n0 ? at0 + static_cast<long long>(p) * step0 : at1 + static_cast<long long>(p - n0) * step1;
+    float v[8][kD];
+    auto fetch = [&](int e0) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float* src = rec_o + __shfl_sync(0xffffffffu, at, min(e0 + e, n - 1)) * HD + lane * kD;
@@ -1047,6 +968,21 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
           v[e][0] = f.x; v[e][1] = f.y;
         }
       }
+    };
+    const float2 ml = rec_ml[at];
+    fetch(0);
+    const bool used = lane < n && (ml.y > 0.f || ml.y != ml.y);  // a part without a key has left no output
+    const float now = fmaxf(M, warp_max(used ? ml.x : -INFINITY));
+    const float z = now == -INFINITY ? 0.f : now, w = used ? ex2(ml.x - z) : 0.f;
+    if (p0 > 0) {
+      const float alpha = now == M ? 1.f : ex2(M - z);
+      L *= alpha;
+#pragma unroll
+      for (int d = 0; d < kD; ++d) acc[d] *= alpha;
+    }
+    M = now;
+    if (used) L += w * ml.y;
+    for (int e0 = 0;;) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float we = __shfl_sync(0xffffffffu, w, min(e0 + e, 31));
@@ -1055,6 +991,8 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
           for (int d = 0; d < kD; ++d) acc[d] = fmaf(we, v[e][d], acc[d]);
         }
       }
+      if ((e0 += 8) >= n) break;
+      fetch(e0);
     }
   }
   L = warp_sum(L);
@@ -1094,25 +1032,27 @@ Shape make_shape(int R, int L, int H, int Hkv, int P, int T) {
   s.requests = s.groups > 1 ? 1 : std::min(R, kRows / (L * s.G));
   s.prefix_tiles = (R + s.requests - 1) / s.requests * s.groups;
   s.prefix_items = (s.prefix_tiles + 1) / 2;
-  s.prefix_blocks = Shape::blocks_of(P);
-  s.prefix_cost = s.prefix_tiles > 1 ? kCostTwo : kCostOne;
   s.own_items = (s.groups + 1) / 2;
-  s.small = L * s.G <= kSmallRows ? (L * s.G + 15) / 16 : 0;
-  s.own_cost = s.small ? kSmallCost : s.groups > 1 ? kCostTwo : kCostOne;
-  s.own_extra = s.small ? kSmallCostItem : kCostItem;
-  s.own_shift = s.small ? kSmallShift : 7;
   s.own_rec = s.tokens * s.G;
   s.prefix_rec = s.requests * s.own_rec;
-  s.grid = sm_count_current();
-  s.own_ctas = s.small == 1 ? 2 * s.grid : s.grid;
-  if (s.small)
-    s.own_ctas = static_cast<int>(std::min<long long>(s.own_ctas, static_cast<long long>(R) * Hkv * ((T + 63) / 64)));
-  s.own_rec0 = P > 0 ? 2 * (static_cast<long long>(Hkv) * s.prefix_items + s.grid) * s.prefix_rec : 0;
+  s.own_small = T > 0 && static_cast<long long>(L) * s.G <= kSmallOwn ? (L * s.G + 15) / 16 : 0;
+  s.prefix_small = P > 0 && static_cast<long long>(R) * L * s.G <= kSmallPrefix;
+  s.prefix_per = s.prefix_small ? 4 : 2;
+  s.own_per = s.own_small ? 4 : 2;
+  s.prefix_blocks = blocks_of(P, s.prefix_small ? kSmallShift : 7);
+  s.own_shift = s.own_small ? kSmallShift : 7;
+  s.prefix_cost = s.prefix_tiles > 1 ? kCostTwo : kCostOne;
+  s.own_cost = s.own_small ? kSmallCost : s.groups > 1 ? kCostTwo : kCostOne;
+  s.own_extra = s.own_small ? kSmallCostItem : kCostItem;
+  const int sms = sm_count_current();
+  auto ctas = [&](int small, long long blocks) { return static_cast<int>(std::min<long long>(small == 1 ? 2 * sms : sms, blocks)); };
+  s.prefix_ctas = ctas(s.prefix_small, static_cast<long long>(Hkv) * s.prefix_items * s.prefix_blocks);
+  s.own_ctas = ctas(s.own_small, static_cast<long long>(R) * Hkv * s.own_items * blocks_of(T, s.own_shift));
+  s.own_rec0 = s.prefix_per * (static_cast<long long>(Hkv) * s.prefix_items + s.prefix_ctas) * s.prefix_rec;
   return s;
 }
 long long record_rows(const Shape& s) {
-  const int per = s.small ? 1 : 2;
-  return s.own_rec0 + (s.T > 0 ? per * (static_cast<long long>(s.R) * s.Hkv * s.own_items + s.own_ctas) * s.own_rec : 0);
+  return s.own_rec0 + s.own_per * (static_cast<long long>(s.R) * s.Hkv * s.own_items + s.own_ctas) * s.own_rec;
 }
 
 // rows as (dimension, head, token, request); boxes of 64 dimensions of heads x tokens x requests
@@ -1126,15 +1066,15 @@ bool row_map(CUtensorMap* m, const void* p, int hd, int heads, int tokens, int r
 }
 
 template <int HD, int MT>
-mtp_status launch_own(const Shape& s, const Maps& m, float scale_log2, float2* ml, float* ro, bool after_prefix, cudaStream_t st) {
+mtp_status launch_small(const Shape& s, const Maps& m, float scale_log2, float2* ml, float* ro, bool after, cudaStream_t st) {
   using C = Small<HD, MT>;
   static PerDevice attr;
-  auto kernel = own_attn_kernel<HD, MT>;
-  if (!smem_limit(attr, kernel, C::kSmemBytes)) return MTP_ERR_CUDA;
-  if (after_prefix)
-    MTP_CUDA_TRY(launch_pdl(kernel, dim3(s.own_ctas), dim3(C::kThreads), C::kSmemBytes, st, m, s, scale_log2, ml, ro, 1));
+  if (!smem_limit(attr, small_attn_kernel<HD, MT>, C::kSmemBytes)) return MTP_ERR_CUDA;
+  const int ctas = std::max(s.prefix_small ? s.prefix_ctas : 0, s.own_small ? s.own_ctas : 0);
+  if (after)
+    MTP_CUDA_TRY(launch_pdl(small_attn_kernel<HD, MT>, dim3(ctas), dim3(C::kThreads), C::kSmemBytes, st, m, s, scale_log2, ml, ro, 1));
   else
-    kernel<<<s.own_ctas, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro, 0);
+    small_attn_kernel<HD, MT><<<ctas, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro, 0);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;
@@ -1146,12 +1086,12 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   static PerDevice attr;
   if (!smem_limit(attr, prefix_attn_kernel<HD>, C::kSmemBytes)) return MTP_ERR_CUDA;
   Maps m{};
+  const int pbox = s.prefix_small ? kSmallBox : 64, box = s.own_small ? kSmallBox : 64;
   if (p.P > 0 &&
       (!row_map(&m.q_prefix, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, s.requests) ||
-       !row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1) ||
-       !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, 64, 1)))
+       !row_map(&m.pk, p.pk, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, pbox, 1) ||
+       !row_map(&m.pv, p.pv, HD, p.Hkv, p.P, 1, p.p_h, p.p_t, p.p_t, 1, pbox, 1)))
     return MTP_ERR_CUDA;
-  const int box = s.small ? kSmallBox : 64;
   if (p.T > 0 &&
       (!row_map(&m.q_own, p.q, HD, p.H, p.L, p.R, p.q_h, p.q_l, p.q_r, s.G, s.tokens, 1) ||
        !row_map(&m.kk, p.kk, HD, p.Hkv, p.T, p.R, p.k_h, p.k_t, p.k_r, 1, box, 1) ||
@@ -1159,22 +1099,23 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
     return MTP_ERR_CUDA;
   const float scale = p.scale > 0.f ? p.scale : 1.0f / sqrtf(static_cast<float>(HD));
   const float scale_log2 = scale * kLog2e;
-  const bool tiles = p.P > 0 || (p.T > 0 && !s.small);
+  const bool tiles = (p.P > 0 && !s.prefix_small) || (p.T > 0 && !s.own_small);
   if (tiles) {
-    prefix_attn_kernel<HD><<<s.grid, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro);
+    const int ctas = std::max(s.prefix_small ? 0 : s.prefix_ctas, s.own_small ? 0 : s.own_ctas);
+    prefix_attn_kernel<HD><<<ctas, C::kThreads, C::kSmemBytes, st>>>(m, s, scale_log2, ml, ro);
     note_launch();
     MTP_LAUNCH_CHECK();
   }
-  if (p.T > 0 && s.small) {
-    const mtp_status e =
-        s.small == 1 ? launch_own<HD, 1>(s, m, scale_log2, ml, ro, tiles, st) : launch_own<HD, 2>(s, m, scale_log2, ml, ro, tiles, st);
+  if (s.prefix_small || s.own_small) {
+    const mtp_status e = std::max(s.prefix_small, s.own_small) == 1 ? launch_small<HD, 1>(s, m, scale_log2, ml, ro, tiles, st)
+                                                                    : launch_small<HD, 2>(s, m, scale_log2, ml, ro, tiles, st);
     if (e != MTP_OK) return e;
   }
-  const dim3 grid((s.L * s.H + 7) / 8, s.R);
+  const dim3 grid((s.L * s.H + kJoinWarps - 1) / kJoinWarps, s.R);
   if (p.P > 0 || p.T > 0)
-    MTP_CUDA_TRY(launch_pdl(prefix_join_kernel<HD>, grid, dim3(256), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
+    MTP_CUDA_TRY(launch_pdl(prefix_join_kernel<HD>, grid, dim3(32 * kJoinWarps), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
   else
-    prefix_join_kernel<HD><<<grid, 256, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
+    prefix_join_kernel<HD><<<grid, 32 * kJoinWarps, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;
