@@ -32,7 +32,7 @@
 //   K warp     walks the deal, publishes the segments in a ring and loads Q and K
 //   V warp     loads V (as a second lane of the K warp it stood still whenever the
 //              first was suspended in a wait: 4 us per short segment)
-//   MMA warp   one thread issues every product
+//   MMA warp   issues every product
 // A last block is loaded as 64 rows where it has no more, and its products run
 // over as many groups of 16 keys as it has.  Keys past a request's ctx_len may
 // hold anything: their scores are replaced, and their V rows are cleared in
@@ -85,7 +85,7 @@ struct Shape {
   int tokens;        // new tokens of a request per row tile (L, or as many as fit)
   int groups;        // token groups per request: ceil(L / tokens)
   int requests;      // requests per row tile of the prefix
-  int prefix_tiles, prefix_items, prefix_blocks, prefix_cost;  // row tiles and items per key head; blocks; cost of one
+  int prefix_tiles, prefix_items, prefix_blocks;  // row tiles and items per key head; blocks
   int prefix_ctas;          // CTAs that share the prefix
   int own_items, own_cost, own_extra;  // row tiles of an own item: `groups` per key head; cost of a block, of an item besides
   int own_shift, own_ctas;  // log2 of a block's keys; CTAs that share the own caches
@@ -96,8 +96,12 @@ struct Shape {
   const int32_t* ctx_len;
 
   __device__ __forceinline__ int ctx(int r) const { return ctx_len ? min(max(ctx_len[r], 0), T) : T; }
-  __host__ __device__ long long prefix_total() const {
-    return static_cast<long long>(Hkv) * prefix_items * prefix_blocks * prefix_cost;
+  // cost of a block of prefix item k of a key head (with one row tile or two), where the item
+  // starts in the head's, and what a head costs
+  __host__ __device__ int prefix_cost(int k) const { return 2 * k + 1 < prefix_tiles ? kCostTwo : kCostOne; }
+  __host__ __device__ long long prefix_at(int k) const { return static_cast<long long>(k) * prefix_blocks * kCostTwo; }
+  __host__ __device__ long long prefix_head() const {
+    return static_cast<long long>(prefix_blocks) * (prefix_tiles / 2 * kCostTwo + prefix_tiles % 2 * kCostOne);
   }
   // blocks of a request's own cache, cost of an item over them, and of all such items of the request
   __device__ __forceinline__ int own_blocks(int r) const { return blocks_of(ctx(r), own_shift); }
@@ -154,10 +158,10 @@ __device__ __forceinline__ bool each_segment(const Shape& sh, int cta, int lane,
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     } else {
-      total = sh.prefix_total();
+      total = sh.Hkv * sh.prefix_head();
     }
-    const int block = kind ? sh.own_cost : sh.prefix_cost, extra = kind ? sh.own_extra : 0;
-    const Deal deal(total, block + extra, kind ? sh.own_ctas : sh.prefix_ctas);
+    const int extra = kind ? sh.own_extra : 0;
+    const Deal deal(total, kind ? sh.own_cost + extra : sh.prefix_cost(0), kind ? sh.own_ctas : sh.prefix_ctas);
     if (total <= 0 || cta >= deal.n) continue;
     const long long from = deal.start(cta), to = deal.start(cta + 1);
     int r = 0;  // request that the range starts in, and where it starts
@@ -183,26 +187,32 @@ __device__ __forceinline__ bool each_segment(const Shape& sh, int cta, int lane,
     for (; r < (kind ? sh.R : 1) && start < to; ++r) {
       const int keys = kind ? sh.ctx(r) : sh.P, nb = kind ? sh.own_blocks(r) : sh.prefix_blocks;
       if (nb == 0) continue;
-      const long long cost = static_cast<long long>(nb) * block + extra;
-      int k = from > start ? static_cast<int>((from - start) / cost) : 0;
+      // items before item k of the request's (of the prefix's), by cost
+      const long long own = kind ? sh.own_item(nb) : 0, head = kind ? own * items : sh.prefix_head();
       Segment s;
-      s.head = k / items;
-      s.item = k - s.head * items;
       s.r = r;
       s.keys = keys;
-      for (long long at = start + k * cost; k < per_r && at < to; ++k, at += cost) {
+      const long long in = from > start ? from - start : 0;
+      s.head = static_cast<int>(in / head);
+      const long long left = in - s.head * head;
+      s.item = static_cast<int>(min(kind ? left / own : left / sh.prefix_at(1), static_cast<long long>(items - 1)));
+      long long at = start + s.head * head + (kind ? s.item * own : sh.prefix_at(s.item));
+      for (int k = s.head * items + s.item; k < per_r && at < to; ++k) {
+        const int block = kind ? sh.own_cost : sh.prefix_cost(s.item);
+        const long long cost = static_cast<long long>(nb) * block + extra;
         // the item's blocks that start in [from, to)
         s.b0 = from <= at ? 0 : Deal::before(from, at, extra, block, nb);
         s.n = (to >= at + cost ? nb : Deal::before(to, at, extra, block, nb)) - s.b0;
         s.kind = kind | (2 * s.item + 1 < tiles ? 2 : 0);
         s.rec = r * per_r + k + cta;
         if (s.n > 0 && !take(s)) return false;
+        at += cost;
         if (++s.item == items) {
           s.item = 0;
           ++s.head;
         }
       }
-      start += cost * per_r;
+      start += head * sh.Hkv;
     }
   }
   return true;
@@ -223,7 +233,7 @@ struct Cfg {
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
   static constexpr int kRing = 8;
-  static constexpr int kReaders = 2 + kSoftmaxWarps;  // V thread, MMA thread, softmax warps
+  static constexpr int kReaders = 2 + kSoftmaxWarps;  // V warp, MMA warp, softmax warps
   // q, k, v full/empty; per tile s_full, p_full, pv_done, o_free; drain; segment ring full/empty
   static constexpr int kNumBars = 2 * (kQTiles + kKStages + kVStages) + 8 + 1 + 2 * kRing;
   static constexpr int kOffRing = (kOffBar + 8 * kNumBars + 15) / 16 * 16;
@@ -306,19 +316,13 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto wait = [&](uint32_t bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, err); };
-  // segment i, read by one thread
   auto peek_segment = [&](uint32_t i, Segment& s) {
     if (!wait(seg_full(i), (i / C::kRing) & 1)) return false;
     const int4 a = ring[2 * (i % C::kRing)], b = ring[2 * (i % C::kRing) + 1];
     s = Segment{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     return s.kind >= 0;
   };
-  auto read_segment = [&](uint32_t i, Segment& s) {
-    if (!peek_segment(i, s)) return false;
-    mbar_arrive1(seg_empty(i));
-    return true;
-  };
-  // ... by a warp: its slot is released once every lane has read it
+  // segment i, read by a warp: its slot is released once every lane has read it
   auto read_segment_warp = [&](uint32_t i, Segment& s) {
     if (!__all_sync(0xffffffffu, peek_segment(i, s))) return false;
     if (lane == 0) mbar_arrive1(seg_empty(i));
@@ -399,13 +403,15 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         wait_drain(q_full(x), (x / C::kQTiles) & 1, kWaitLimitCycles);
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issuer ----------------
-    if (lane == 0) {
+    // The whole warp walks along, so that what a product is given is uniform.
+    {
       constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
       uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
       uint32_t turn = 0;            // blocks with one row tile so far: the TMEM tile is its parity
       uint32_t ns[2] = {0u, 0u};    // S products issued per TMEM tile
       uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose first P V has been issued
       bool ok = true, any = false;
+      auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
       // groups of 16 keys in block b of a segment's item
       auto groups16 = [&](const Segment& s, int b) { return (min(s.keys - b * kKeys, kKeys) + 15) / 16; };
       // S_x = Q K^T of row tile `qt` and ring block gu; the P that shared its columns was read by a
@@ -417,38 +423,43 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t off = (k >> 2) * C::kPiece + (k & 3) * 32;
-          umma_bf16_ss(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
+          umma_bf16_ss_warp(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
         }
-        umma_commit(s_full(x));
+        umma_commit_warp(s_full(x));
         ++ns[x];
         any = true;
       };
-      auto wait_q = [&](uint32_t qt) { return wait(q_full(qt), (qt / C::kQTiles) & 1); };
+      auto wait_q = [&](uint32_t qt) { return wwait(q_full(qt), (qt / C::kQTiles) & 1); };
       auto wait_k = [&](uint32_t gu) {
-        if (!wait(k_full(gu), (gu / C::kKStages) & 1)) return false;
+        if (!wwait(k_full(gu), (gu / C::kKStages) & 1)) return false;
         tc_fence_after();
         return true;
       };
       // O_x (+)= P_x V of ring block gu, P_x from tile x's last S
       auto issue_pv = [&](int x, uint32_t gu, int keys16, bool first) {
-        if (!wait(p_full(x), (ns[x] - 1) & 1)) return false;
+        if (!wwait(p_full(x), (ns[x] - 1) & 1)) return false;
         if (first) {
-          if (no[x] > 0 && !wait(o_free(x), (no[x] - 1) & 1)) return false;
+          if (no[x] > 0 && !wwait(o_free(x), (no[x] - 1) & 1)) return false;
           ++no[x];
         }
         tc_fence_after();
         const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k) {
-          if (k >= keys16) break;
+        auto product = [&](int k) {
           const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
-          umma_bf16_ts(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
-                       (!first || k > 0) ? 1u : 0u);
+          umma_bf16_ts_warp(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
+                            (!first || k > 0) ? 1u : 0u);
+        };
+        if (keys16 == kKeys / 16) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k) product(k);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < keys16; ++k) product(k);
         }
-        umma_commit(pv_done(x));
+        umma_commit_warp(pv_done(x));
         return true;
       };
-      auto wait_v = [&](uint32_t gu) { return wait(v_full(gu), (gu / C::kVStages) & 1); };
+      auto wait_v = [&](uint32_t gu) { return wwait(v_full(gu), (gu / C::kVStages) & 1); };
       // with one row tile: the product of the block whose S was issued last waits until the
       // next block's S (of the other TMEM tile, of the next segment too) has been issued
       bool pending = false, pending_first = false;
@@ -458,12 +469,15 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         if (!pending) return true;
         pending = false;
         if (!wait_v(pending_g) || !issue_pv(pending_x, pending_g, pending_keys, pending_first)) return false;
-        umma_commit(v_empty(pending_g));
+        umma_commit_warp(v_empty(pending_g));
         return true;
       };
       Segment s;
-      for (uint32_t i = 0; ok && read_segment(i, s); ++i) {
-        const int n = s.n;
+      for (uint32_t i = 0; ok && read_segment_warp(i, s); ++i) {
+        s.kind = __shfl_sync(0xffffffffu, s.kind, 0);
+        s.b0 = __shfl_sync(0xffffffffu, s.b0, 0);
+        s.keys = __shfl_sync(0xffffffffu, s.keys, 0);
+        const int n = __shfl_sync(0xffffffffu, s.n, 0);
         if (!(s.kind & 2)) {
           if (!wait_q(tile)) { ok = false; break; }
           for (int j = 0; j < n && ok; ++j, ++turn, ++g) {
@@ -471,8 +485,8 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
             if (!wait_k(g)) { ok = false; break; }
             const int keys16 = groups16(s, s.b0 + j);
             issue_s(x, tile, g, keys16);
-            umma_commit(k_empty(g));
-            if (j + 1 == n) umma_commit(q_empty(tile));
+            umma_commit_warp(k_empty(g));
+            if (j + 1 == n) umma_commit_warp(q_empty(tile));
             if (!flush()) { ok = false; break; }
             pending = true;
             pending_x = x;
@@ -485,14 +499,15 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           if (!flush() || !wait_q(tile) || !wait_q(tile + 1) || !wait_k(g)) { ok = false; break; }
           issue_s(0, tile, g, groups16(s, s.b0));
           issue_s(1, tile + 1, g, groups16(s, s.b0));
-          umma_commit(k_empty(g));
+          umma_commit_warp(k_empty(g));
           for (int j = 0; j < n && ok; ++j) {
             const uint32_t gu = g + j;
             if (j + 1 == n) {
-              umma_commit(q_empty(tile));
-              umma_commit(q_empty(tile + 1));
+              umma_commit_warp(q_empty(tile));
+              umma_commit_warp(q_empty(tile + 1));
             }
             if (!wait_v(gu)) { ok = false; break; }
+#pragma unroll 1
             for (int x = 0; x < 2 && ok; ++x) {
               if (!issue_pv(x, gu, groups16(s, s.b0 + j), j == 0)) { ok = false; break; }
               if (j + 1 < n) {
@@ -501,8 +516,8 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
               }
             }
             if (!ok) break;
-            umma_commit(v_empty(gu));
-            if (j + 1 < n) umma_commit(k_empty(gu + 1));
+            umma_commit_warp(v_empty(gu));
+            if (j + 1 < n) umma_commit_warp(k_empty(gu + 1));
           }
           g += n;
           tile += 2;
@@ -511,7 +526,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
       if (ok) flush();
       // every issued MMA has completed before TMEM is freed
       if (any) {
-        umma_commit(drain_bar);
+        umma_commit_warp(drain_bar);
         wait_drain(drain_bar, 0, kWaitLimitCycles);
       }
     }
@@ -911,12 +926,12 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
   long long at0 = 0, at1 = 0;
   int n0 = 0, n1 = 0, step0 = 0, step1 = 0;
   if (sh.prefix_blocks > 0) {
-    const Deal shared(sh.prefix_total(), sh.prefix_cost, sh.prefix_ctas);
+    const Deal shared(sh.Hkv * sh.prefix_head(), sh.prefix_cost(0), sh.prefix_ctas);
     const int tile = r / sh.requests * sh.groups + group, row = r % sh.requests * sh.tokens * sh.G + in;
     const bool two = (tile | 1) < sh.prefix_tiles;
     const int k = head * sh.prefix_items + tile / 2;
-    const long long cost = static_cast<long long>(sh.prefix_blocks) * sh.prefix_cost, at = k * cost;
-    const int a = shared.owner(at), b = shared.owner(at + cost - sh.prefix_cost);
+    const long long at = head * sh.prefix_head() + sh.prefix_at(tile / 2);
+    const int a = shared.owner(at), b = shared.owner(at + static_cast<long long>(sh.prefix_blocks - 1) * sh.prefix_cost(tile / 2));
     // two row tiles leave a part each and this row has every other one, else they are all this row's
     n0 = (b - a + 1) * (two ? 1 : sh.prefix_per);
     step0 = (two ? 2 : 1) * sh.prefix_rec;
@@ -1041,7 +1056,6 @@ Shape make_shape(int R, int L, int H, int Hkv, int P, int T) {
   s.own_per = s.own_small ? 4 : 2;
   s.prefix_blocks = blocks_of(P, s.prefix_small ? kSmallShift : 7);
   s.own_shift = s.own_small ? kSmallShift : 7;
-  s.prefix_cost = s.prefix_tiles > 1 ? kCostTwo : kCostOne;
   s.own_cost = s.own_small ? kSmallCost : s.groups > 1 ? kCostTwo : kCostOne;
   s.own_extra = s.own_small ? kSmallCostItem : kCostItem;
   const int sms = sm_count_current();
