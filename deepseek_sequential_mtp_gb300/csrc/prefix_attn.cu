@@ -403,132 +403,102 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         wait_drain(q_full(x), (x / C::kQTiles) & 1, kWaitLimitCycles);
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issuer ----------------
-    // The whole warp walks along, so that what a product is given is uniform.
-    {
-      constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
-      uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
-      uint32_t turn = 0;            // blocks with one row tile so far: the TMEM tile is its parity
-      uint32_t ns[2] = {0u, 0u};    // S products issued per TMEM tile
-      uint32_t no[2] = {0u, 0u};    // segments per TMEM tile whose first P V has been issued
-      bool ok = true, any = false;
-      auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
-      // groups of 16 keys in block b of a segment's item
-      auto groups16 = [&](const Segment& s, int b) { return (min(s.keys - b * kKeys, kKeys) + 15) / 16; };
-      // S_x = Q K^T of row tile `qt` and ring block gu; the P that shared its columns was read by a
-      // product issued before
-      auto issue_s = [&](int x, uint32_t qt, uint32_t gu, int keys16) {
+    // The whole warp walks along, so that what a product is given is uniform.  The row tiles'
+    // blocks form one sequence, which takes the TMEM tiles alternately: S of a step, then P V
+    // of the step before, whose softmax ran meanwhile.
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kRows, HD, 2);  // V read MN-major, P from TMEM
+    auto wwait = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    uint32_t g = 0, tile = 0;     // key blocks and Q tiles consumed
+    uint32_t turn = 0;            // blocks with one row tile so far: the TMEM tile is its parity
+    // a bit per TMEM tile: parity of the S products issued; of the segments whose first P V has
+    // been issued, and whether there are any
+    uint32_t ns = 0, no = 0, had = 0;
+    uint32_t i = 0;
+    Segment s{};
+    int tiles = 1, j = 0, t = 0;  // row tiles of the segment; block and row tile of the next step
+    bool more = true, any = false;
+    // the step whose P V is due: TMEM tile, ring block, groups of 16 keys, whether it is the segment's
+    // first on that TMEM tile, and the block's last row tile
+    bool due = false, due_first = false, due_last = false;
+    int due_x = 0, due_keys = 0;
+    uint32_t due_g = 0;
+    while (more || due) {
+      if (more && j == s.n) {
+        more = read_segment_warp(i++, s);
+        s.kind = __shfl_sync(0xffffffffu, s.kind, 0);
+        s.b0 = __shfl_sync(0xffffffffu, s.b0, 0);
+        s.n = __shfl_sync(0xffffffffu, s.n, 0);
+        s.keys = __shfl_sync(0xffffffffu, s.keys, 0);
+        tile += i > 1 ? tiles : 0;
+        tiles = s.kind & 2 ? 2 : 1;
+        j = 0;
+      }
+      const int x = tiles == 2 ? t : turn & 1;
+      const int keys16 = (min(s.keys - (s.b0 + j) * kKeys, kKeys) + 15) / 16;
+      const bool now = more && !(due && due_x == x);  // P of a due step may still be in S's columns
+      if (now) {
+        const uint32_t qt = tile + t;
+        if (j == 0 && !wwait(q_full(qt), (qt / C::kQTiles) & 1)) break;
+        if (t == 0 && !wwait(k_full(g), (g / C::kKStages) & 1)) break;
+        tc_fence_after();
         const uint32_t idesc_s = idesc_bf16_f32(kRows, 16 * keys16, 0);
-        const uint32_t q_at = sQ + (qt % C::kQTiles) * C::kTileBytes;
-        const uint32_t k_at = sK + (gu % C::kKStages) * C::kTileBytes;
+        const uint32_t q_at = sQ + (qt % C::kQTiles) * C::kTileBytes, k_at = sK + (g % C::kKStages) * C::kTileBytes;
 #pragma unroll
         for (int k = 0; k < HD / 16; ++k) {
           const uint32_t off = (k >> 2) * C::kPiece + (k & 3) * 32;
           umma_bf16_ss_warp(tmem + 128u * x, sdesc_k_sw128(q_at + off), sdesc_k_sw128(k_at + off), idesc_s, k > 0);
         }
         umma_commit_warp(s_full(x));
-        ++ns[x];
+        ns ^= 1u << x;
         any = true;
-      };
-      auto wait_q = [&](uint32_t qt) { return wwait(q_full(qt), (qt / C::kQTiles) & 1); };
-      auto wait_k = [&](uint32_t gu) {
-        if (!wwait(k_full(gu), (gu / C::kKStages) & 1)) return false;
-        tc_fence_after();
-        return true;
-      };
-      // O_x (+)= P_x V of ring block gu, P_x from tile x's last S
-      auto issue_pv = [&](int x, uint32_t gu, int keys16, bool first) {
-        if (!wwait(p_full(x), (ns[x] - 1) & 1)) return false;
-        if (first) {
-          if (no[x] > 0 && !wwait(o_free(x), (no[x] - 1) & 1)) return false;
-          ++no[x];
+        if (t + 1 == tiles) umma_commit_warp(k_empty(g));
+        if (j + 1 == s.n) umma_commit_warp(q_empty(qt));
+      }
+      if (due) {
+        if (!wwait(v_full(due_g), (due_g / C::kVStages) & 1)) break;
+        // P of this TMEM tile's last S but for the one just issued
+        if (!wwait(p_full(due_x), ~ns >> due_x & 1)) break;
+        if (due_first) {
+          if ((had >> due_x & 1) && !wwait(o_free(due_x), ~no >> due_x & 1)) break;
+          no ^= 1u << due_x;
+          had |= 1u << due_x;
         }
         tc_fence_after();
-        const uint32_t v_at = sV + (gu % C::kVStages) * C::kTileBytes;
+        const uint32_t v_at = sV + (due_g % C::kVStages) * C::kTileBytes;
         auto product = [&](int k) {
           const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
-          umma_bf16_ts_warp(tmem + C::kColO + HD * x, tmem + 128u * x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
-                            (!first || k > 0) ? 1u : 0u);
+          umma_bf16_ts_warp(tmem + C::kColO + HD * due_x, tmem + 128u * due_x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
+                            (!due_first || k > 0) ? 1u : 0u);
         };
-        if (keys16 == kKeys / 16) {
+        if (due_keys == kKeys / 16) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k) product(k);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < keys16; ++k) product(k);
+          for (int k = 0; k < due_keys; ++k) product(k);
         }
-        umma_commit_warp(pv_done(x));
-        return true;
-      };
-      auto wait_v = [&](uint32_t gu) { return wwait(v_full(gu), (gu / C::kVStages) & 1); };
-      // with one row tile: the product of the block whose S was issued last waits until the
-      // next block's S (of the other TMEM tile, of the next segment too) has been issued
-      bool pending = false, pending_first = false;
-      int pending_x = 0, pending_keys = 0;
-      uint32_t pending_g = 0;
-      auto flush = [&]() {
-        if (!pending) return true;
-        pending = false;
-        if (!wait_v(pending_g) || !issue_pv(pending_x, pending_g, pending_keys, pending_first)) return false;
-        umma_commit_warp(v_empty(pending_g));
-        return true;
-      };
-      Segment s;
-      for (uint32_t i = 0; ok && read_segment_warp(i, s); ++i) {
-        s.kind = __shfl_sync(0xffffffffu, s.kind, 0);
-        s.b0 = __shfl_sync(0xffffffffu, s.b0, 0);
-        s.keys = __shfl_sync(0xffffffffu, s.keys, 0);
-        const int n = __shfl_sync(0xffffffffu, s.n, 0);
-        if (!(s.kind & 2)) {
-          if (!wait_q(tile)) { ok = false; break; }
-          for (int j = 0; j < n && ok; ++j, ++turn, ++g) {
-            const int x = turn & 1;
-            if (!wait_k(g)) { ok = false; break; }
-            const int keys16 = groups16(s, s.b0 + j);
-            issue_s(x, tile, g, keys16);
-            umma_commit_warp(k_empty(g));
-            if (j + 1 == n) umma_commit_warp(q_empty(tile));
-            if (!flush()) { ok = false; break; }
-            pending = true;
-            pending_x = x;
-            pending_keys = keys16;
-            pending_g = g;
-            pending_first = j < 2;  // the segment's first block on this TMEM tile
-          }
-          ++tile;
-        } else {
-          if (!flush() || !wait_q(tile) || !wait_q(tile + 1) || !wait_k(g)) { ok = false; break; }
-          issue_s(0, tile, g, groups16(s, s.b0));
-          issue_s(1, tile + 1, g, groups16(s, s.b0));
-          umma_commit_warp(k_empty(g));
-          for (int j = 0; j < n && ok; ++j) {
-            const uint32_t gu = g + j;
-            if (j + 1 == n) {
-              umma_commit_warp(q_empty(tile));
-              umma_commit_warp(q_empty(tile + 1));
-            }
-            if (!wait_v(gu)) { ok = false; break; }
-#pragma unroll 1
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (!issue_pv(x, gu, groups16(s, s.b0 + j), j == 0)) { ok = false; break; }
-              if (j + 1 < n) {
-                if (x == 0 && !wait_k(gu + 1)) { ok = false; break; }
-                issue_s(x, tile + x, gu + 1, groups16(s, s.b0 + j + 1));
-              }
-            }
-            if (!ok) break;
-            umma_commit_warp(v_empty(gu));
-            if (j + 1 < n) umma_commit_warp(k_empty(gu + 1));
-          }
-          g += n;
-          tile += 2;
+        umma_commit_warp(pv_done(due_x));
+        if (due_last) umma_commit_warp(v_empty(due_g));
+      }
+      due = now;
+      if (now) {
+        due_x = x;
+        due_keys = keys16;
+        due_g = g;
+        due_first = tiles == 2 ? j == 0 : j < 2;
+        due_last = t + 1 == tiles;
+        if (tiles == 1) ++turn;
+        if (++t == tiles) {
+          t = 0;
+          ++j;
+          ++g;
         }
       }
-      if (ok) flush();
-      // every issued MMA has completed before TMEM is freed
-      if (any) {
-        umma_commit_warp(drain_bar);
-        wait_drain(drain_bar, 0, kWaitLimitCycles);
-      }
+    }
+    // every issued MMA has completed before TMEM is freed
+    if (any) {
+      umma_commit_warp(drain_bar);
+      wait_drain(drain_bar, 0, kWaitLimitCycles);
     }
   } else {
     // ---------------- softmax: one row per thread of tile x ----------------
