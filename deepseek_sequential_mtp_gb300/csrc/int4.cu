@@ -1,7 +1,9 @@
 // 4-bit weight GEMM for 1..32 tokens: out[r, n] = Σ_k x[r, k] (q[n, k] - zero[n, k/G]) scale[n, k/G].
 //
 // Bound: HBM, half a byte per weight; what has to keep up with it is the
-// unpacking.  The products run on mma.sync.m16n8k16 with 16 weight rows as the
+// unpacking.  18432 x 7168, groups of 128: one token 21 us (3.4 TB/s), 8 tokens 27,
+// 32 tokens 43 (bound by the tokens' share of the work: mma.sync at its rate alone
+// takes 15); 73728 x 7168, one token 62 us (4.6 TB/s).  The products run on mma.sync.m16n8k16 with 16 weight rows as the
 // A operand and 8 tokens as B: (q - zero) is an integer of at most 5 bits, so
 // it is exact in bf16, the products with bf16 activations are exact in fp32
 // and a group's sum is multiplied by its scale in fp32 -- nothing is rounded
@@ -45,19 +47,21 @@ constexpr int kMaxTokens = 32;
 
 // Variants by the number of 8-token tiles NT: with more than one, one CTA of 16
 // warps per SM shares the staged activations (16 tokens, 18432 x 7168: 28 us;
-// two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47), with one, three of 8.
+// two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47).  With one, the
+// fixed part of a step weighs more: two CTAs of 8 warps and 256 weights of a row
+// per step (one token, 73728 x 7168: 62 us; three CTAs and 128 weights 72).
 template <int NT> struct Cfg {
   static constexpr int kChunk = NT > 1 ? 128 : 256;       // weights of a row per step
   static constexpr int kUnitBytes = 2 * kChunk;           // a token's activations of one chunk
   static constexpr int kWords = kChunk / 32;              // words of a row per lane
   static constexpr int kWarps = NT > 1 ? 16 : 8;
-  static constexpr int kCtas = NT > 1 ? 1 : 2;      // per SM
-  static constexpr int kDepth = 4;  // chunks of weights in flight per warp
+  static constexpr int kCtas = NT > 1 ? 1 : 2;            // per SM
+  static constexpr int kDepth = 4;                        // chunks of weights in flight per warp
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kSlotBytes = kChunk * 8;           // a warp's chunk: 16 bytes per lane, row and 128 weights
-  static constexpr int kRingSlots = kDepth <= 4 ? 4 : 8;  // a power of two: slots by mask
+  static constexpr int kRingSlots = kDepth;               // a power of two: slots by mask
   static constexpr int kRingBytes = kWarps * kRingSlots * kSlotBytes;
-  static constexpr int kSmem = (kCtas == 1 ? 224 : kCtas == 2 ? 112 : kCtas == 3 ? 74 : 55) * 1024;
+  static constexpr int kSmem = 224 / kCtas * 1024;
 };
 
 struct Seg {

@@ -7,36 +7,59 @@
 // and the parts joined at the end: o = Σ 2^(m_p - M) o_p / Σ 2^(m_p - M) l_p.
 //
 // Bound: HBM for few rows (the keys and values once: 4 hd bytes per key and
-// head), the tensor cores once some 300 rows share a head's prefix.
+// head), the tensor cores once some 300 rows share a head's prefix.  Measured, call
+// after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
+// to 256 own keys 79 us (4.4 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
+// 65 us (4.1 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
+// to 512 own keys 63 us (350 TFLOP/s).  Each further key of such a prefix costs its
+// bytes at 6.6 TB/s in the first case, at 5.4 in the second, and 900 TFLOP/s in the
+// third; the rest is three kernels' way to their first data, one after the other.
 //
 // All rows that see the same keys form one matrix: for the prefix the R L G rows
 // (G = query heads per key head) of all requests, for a request's own cache its
-// L G rows.  A row tile is as many whole requests as fit into 128 rows (or, with
-// L G > 128, as many whole tokens of one request), so that one TMA box brings its
-// q.  Work is cut into items -- (key head, one or two row tiles) over the prefix,
-// (request, key head, one or two row tiles) over its cache -- and an item into
-// blocks of 128 keys.  The blocks of all items, weighted by their cost, are dealt
-// to the CTAs in equal contiguous ranges, whatever the lengths; a CTA's range
-// within an item (a segment) leaves one record of partial results per row, and a
-// second kernel joins a row's records.  Both kernels work the deal out from ctx_len.
+// L G rows.  Work is cut into items -- (key head, rows) over the prefix, (request,
+// key head, rows) over its cache -- and an item into blocks of keys.  The blocks of
+// all items, weighted by their cost, are dealt to the CTAs in equal contiguous
+// ranges, whatever the lengths; a CTA's range within an item (a segment) leaves
+// records of partial results for each row, and a last kernel joins a row's records.
+// Every kernel works the deal out from ctx_len.
 //
-// A segment runs as in the chain's attention: TMA brings Q, K and V blocks, S =
-// Q K^T and O += P V run on tcgen05 with S, P and O in TMEM, a softmax thread owns
-// a row.  TMEM holds two tiles (S and P share columns), each with its own
-// warpgroup.  With two row tiles both share every K/V block.  With one, the TMEM
-// tiles take the blocks alternately, so that one's softmax runs under the other's
-// products, each with a maximum, a sum and an output of its own (two records);
-// the alternation runs on from segment to segment, so that short segments overlap
-// as well.
+// Many rows (prefix_attn_kernel): a row tile is as many whole requests as fit into
+// 128 rows (or, with L G > 128, as many whole tokens of one request), so that one
+// TMA box brings its q; an item has one or two row tiles, a block 128 keys.  TMA
+// brings Q, K and V blocks, S = Q K^T and O += P V run on tcgen05 with S, P and O in
+// TMEM, a softmax thread owns a row.  TMEM holds two tiles (S and P share columns),
+// each with its own warpgroup.  With two row tiles both share every K/V block.  With
+// one, the TMEM tiles take the blocks alternately, so that one's softmax runs under
+// the other's products, each with a maximum, a sum and an output of its own (two
+// records); the alternation runs on from segment to segment, so that short segments
+// overlap as well.
 //   softmax    warps 0-3 TMEM tile 0, warps 4-7 tile 1
 //   K warp     walks the deal, publishes the segments in a ring and loads Q and K
 //   V warp     loads V (as a second lane of the K warp it stood still whenever the
 //              first was suspended in a wait: 4 us per short segment)
 //   MMA warp   issues every product
-// A last block is loaded as 64 rows where it has no more, and its products run
-// over as many groups of 16 keys as it has.  Keys past a request's ctx_len may
-// hold anything: their scores are replaced, and their V rows are cleared in
-// shared memory (0 times NaN is NaN).  Every wait is bounded.
+// A last block is loaded as 64 rows where it has no more, and its products run over
+// as many groups of 16 keys as it has.
+//
+// Few rows (small_attn_kernel): own caches with up to 32 rows per key head, and a
+// prefix with up to 16 in all.  The kernel above spends 3.5 us on an item of one or
+// two blocks, whatever its rows: the chain load, S, softmax, P V has two tiles to
+// overlap with, and most of each is padding.  Here a warp takes 16 rows and 16 keys
+// with mma.sync.m16n8k16, and as many chains run as there are warps.  Calls with own
+// caches alone, against the kernel above: 32 requests, 56 heads, 256 keys 59 us
+// instead of 83, 32 heads over 8 with 5 tokens (20 rows), 512 keys 32 instead of 42,
+// 64 over 8 with 4 (32 rows) 37 instead of 43, 2048 keys 76 instead of 78; a prefix
+// of 8192 keys and 16 rows 63 instead of 65, of 300 keys and 4 rows 13.4 instead of
+// 15.5.  A prefix with 32 rows gains nothing (52 us both), own caches with more rows
+// have tiles to fill.  It is launched beside the kernel above, whose CTAs fill an SM,
+// and takes the SMs as they become free.
+//
+// Keys past a request's ctx_len may hold anything: their scores are replaced, and
+// their V rows are cleared in shared memory (0 times NaN is NaN).  P is rounded to
+// bf16 for the second product (half a step, 2^-9 of each weight: as much again as
+// the output's own rounding, 1.4 of it together); statistics, sums and records are
+// fp32.  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>
@@ -895,17 +918,23 @@ small_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale
   if (after) pdl_wait();  // complete only once the kernel before is, which it may run beside
 }
 
-// Joins the records of one (request, token, head) per warp: a lane per record for the
-// maxima and the weights, then lanes over the head's dimensions.  The deals come from
+// Joins the records of one (request, token, head) per warp, or with kSplit = 4 per CTA,
+// each warp every fourth of them: a lane per record for the maxima and the weights, then
+// lanes over the head's dimensions.  The deals come from
 // ctx_len alone, so all of that runs under the kernels before; what is left then is one
 // chain of loads, in which the first records' outputs are asked for with their maxima.
 constexpr int kJoinWarps = 4;
-template <int HD>
+// Up to this many rows per SM have a CTA each: with 128 rows of 150 records a call takes 72 us
+// instead of 85, with 512 of 60 36 instead of 40; with 1792 of 12 111 instead of 108, with 5120 of
+// 20 85 instead of 75.
+constexpr int kSplitRows = 8;
+template <int HD, int kSplit>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const float* __restrict__ rec_o,
                    __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y, item = blockIdx.x * kJoinWarps + warp;
+  static_assert(kSplit == 1 || kSplit == kJoinWarps, "a row per warp, or per CTA");
+  const int r = blockIdx.y, item = kSplit > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
   if (item >= sh.L * sh.H) {
     pdl_wait();
     return;
@@ -951,14 +980,14 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
     at1 = sh.own_rec0 +
           (static_cast<long long>(sh.own_per) * (r * sh.Hkv * sh.own_items + k + a) + (two ? group & 1 : 0)) * sh.own_rec + in;
   }
-  const int parts = n0 + n1;
+  const int w0 = kSplit > 1 ? warp : 0, parts = (n0 + n1 - w0 + kSplit - 1) / kSplit;  // this warp's
   constexpr int kD = HD / 32;
   float acc[kD], L = 0.f, M = -INFINITY;  // L: this lane's records
 #pragma unroll
   for (int d = 0; d < kD; ++d) acc[d] = 0.f;
   pdl_wait();  // the records are earlier kernels'
   for (int p0 = 0; p0 < parts; p0 += 32) {
-    const int p = min(p0 + lane, parts - 1), n = min(32, parts - p0);
+    const int p = min(p0 + lane, parts - 1) * kSplit + w0, n = min(32, parts - p0);
     const long long at = p < n0 ? at0 + static_cast<long long>(p) * step0 : at1 + static_cast<long long>(p - n0) * step1;
     float v[8][kD];
     auto fetch = [&](int e0) {
@@ -1001,6 +1030,30 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
     }
   }
   L = warp_sum(L);
+  if constexpr (kSplit > 1) {
+    __shared__ float s_m[kSplit], s_l[kSplit], s_o[kSplit][HD];
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+#pragma unroll
+    for (int d = 0; d < kD; ++d) s_o[warp][lane * kD + d] = acc[d];
+    __syncthreads();
+    if (warp != 0) return;
+    L = 0.f;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) M = fmaxf(M, s_m[w]);
+    const float z = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int w = 0; w < kSplit; ++w) {
+      const float f = ex2(s_m[w] - z);
+      L += f * s_l[w];
+#pragma unroll
+      for (int d = 0; d < kD; ++d) acc[d] += f * s_o[w][lane * kD + d];
+    }
+  }
   const long long out = (static_cast<long long>(r) * sh.L + i) * sh.H + h;
   if (rec) {
     float* to = rec + out * rec_stride;
@@ -1115,11 +1168,14 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
                                                                     : launch_small<HD, 2>(s, m, scale_log2, ml, ro, tiles, st);
     if (e != MTP_OK) return e;
   }
-  const dim3 grid((s.L * s.H + kJoinWarps - 1) / kJoinWarps, s.R);
+  // few rows: their records by four warps each
+  const bool split = static_cast<long long>(s.R) * s.L * s.H <= kSplitRows * sm_count_current();
+  const dim3 grid(split ? s.L * s.H : (s.L * s.H + kJoinWarps - 1) / kJoinWarps, s.R);
+  auto join = split ? prefix_join_kernel<HD, kJoinWarps> : prefix_join_kernel<HD, 1>;
   if (p.P > 0 || p.T > 0)
-    MTP_CUDA_TRY(launch_pdl(prefix_join_kernel<HD>, grid, dim3(32 * kJoinWarps), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
+    MTP_CUDA_TRY(launch_pdl(join, grid, dim3(32 * kJoinWarps), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
   else
-    prefix_join_kernel<HD><<<grid, 32 * kJoinWarps, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
+    join<<<grid, 32 * kJoinWarps, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;
