@@ -57,9 +57,9 @@
 //
 // Keys past a request's ctx_len may hold anything: their scores are replaced, and
 // their V rows are cleared in shared memory (0 times NaN is NaN).  P is rounded to
-// bf16 for the second product (half a step, 2^-9 of each weight: as much again as
-// the output's own rounding, 1.4 of it together); statistics, sums and records are
-// fp32.  Every wait is bounded.
+// bf16 for the second product (half a step, 2^-8 of each weight at most; over many
+// keys as much as the output's own rounding, 1.4 of it together); statistics, sums
+// and records are fp32.  Every wait is bounded.
 #include <cuda.h>
 
 #include <algorithm>

@@ -199,3 +199,68 @@ def test_refusals():
                dict(q=a["q"].cpu()), dict(q=z(2, 1, 4, 68)[..., :64])):
         with pytest.raises(lib.MtpError):
             lib.prefix_attention(**{**a, "ctx_len": ctx, **kw})
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("R,L,H,Hkv,P,T,ctx", [
+    (8, 1, 4, 2, 1000, 65, [1, 16, 17, 32, 33, 63, 64, 65]),   # 16 rows on the prefix, every tail of a block
+    (17, 1, 2, 2, 300, 40, None),                  # 17 rows: the prefix on row tiles, the own caches not
+    (3, 16, 2, 2, 50, 700, [16, 31, 700]),         # 16 rows per own item, many blocks
+    (3, 17, 2, 2, 50, 700, [17, 300, 699]),        # 17: two tiles of 16 rows
+    (2, 8, 8, 2, 0, 400, [8, 400]),                # 32 rows, no prefix
+    (2, 11, 6, 2, 0, 400, [12, 399]),              # 33 rows
+    (1, 1, 3, 1, 20000, 3000, [2999]),             # one request over all CTAs
+    (150, 1, 2, 1, 64, 200, None),                 # more requests than lanes, items cut anywhere
+    (1, 32, 1, 1, 0, 33, [20]),                    # fewer own rows than new tokens
+])
+def test_few_rows(hd, R, L, H, Hkv, P, T, ctx):
+    a = _inputs(R, L, H, Hkv, hd, P, T, 7 * R + L + P + T)
+    if ctx is None:
+        ctx = [0 if r % 11 == 5 else 1 + (53 * r) % T for r in range(R)]
+    _check(a, ctx, _run(a, ctx))
+
+
+def test_few_rows_past_the_length_hold_anything():
+    for L, H in ((1, 2), (5, 8), (16, 4)):  # 1, 20 and 32 rows per own item
+        a = _inputs(3, L, H, 2, 128, 100, 310, 15)
+        ctx = [L, 129 + L, 300]
+        want = _run(a, ctx)
+        for r in range(3):
+            a["kv_k"][r, ctx[r]:] = float("inf")
+            a["kv_v"][r, ctx[r]:] = float("nan")
+        got = _run(a, ctx)
+        assert torch.equal(got["o"], want["o"]) and torch.equal(got["lse"], want["lse"])
+
+
+def test_no_wait_runs_out():
+    """A wait that runs into its limit takes more than a second; these calls take
+    some 0.1 ms, on every kernel and with rings that are filled many times."""
+    for R, L, H, Hkv, P, T in ((32, 1, 56, 56, 8192, 256), (4, 1, 8, 8, 20000, 3000), (8, 5, 16, 4, 0, 3000), (3, 20, 16, 4, 4000, 900)):
+        a = {k: v.cuda() for k, v in _inputs(R, L, H, Hkv, 128, P, T, 16).items()}
+        lib.prefix_attention(**a)
+        torch.cuda.synchronize()
+        t0, t1 = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        t0.record()
+        lib.prefix_attention(**a)
+        t1.record()
+        torch.cuda.synchronize()
+        assert t0.elapsed_time(t1) < 100, t0.elapsed_time(t1)
+    lib.check_errors()
+
+
+def test_two_calls_at_once():
+    """Calls of both kernels side by side on two streams, each with its own workspace."""
+    a = {k: v.cuda() for k, v in _inputs(6, 2, 8, 4, 128, 3000, 500, 17).items()}
+    b = {k: v.cuda() for k, v in _inputs(24, 5, 8, 2, 128, 2000, 300, 18).items()}
+    want = [lib.prefix_attention(**x) for x in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(6):
+        for i, x in enumerate((a, b)):
+            got[i].append(lib.prefix_attention(**x, stream=streams[i]))
+    torch.cuda.synchronize()
+    lib.check_errors()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g["o"], want[i]["o"]) and torch.equal(g["lse"], want[i]["lse"])
