@@ -421,8 +421,6 @@ extern "C" mtp_status mtp_logits_probs(int R, int L, int V, int dtype, const voi
   if ((reinterpret_cast<uintptr_t>(logits) % esize) || (reinterpret_cast<uintptr_t>(p) & 3u) ||
       (reinterpret_cast<uintptr_t>(status) & 3u))
     return MTP_ERR_ALIGNMENT;
-  // the rows may be rewritten in place, but not through another row's logits
-  if (static_cast<const void*>(p) == logits && (dtype != MTP_F32 || ld != V)) return MTP_ERR_INVALID_ARG;
   Args a{};
   if (prm) a.prm = *prm;
   const mtp_logits_params& q = a.prm;
@@ -439,6 +437,11 @@ extern "C" mtp_status mtp_logits_probs(int R, int L, int V, int dtype, const voi
     if (reinterpret_cast<uintptr_t>(ptr) & 3u) return MTP_ERR_ALIGNMENT;
   const long long rows = static_cast<long long>(R) * L;
   if (rows > 0x7FFFFFFFll / kMaxCluster) return MTP_ERR_UNSUPPORTED;
+  // the rows may be rewritten in place, but not through another row's logits
+  const uintptr_t l0 = reinterpret_cast<uintptr_t>(logits), p0 = reinterpret_cast<uintptr_t>(p);
+  if (ld > 1ll << 33) return MTP_ERR_UNSUPPORTED;
+  const uintptr_t l1 = l0 + (static_cast<uintptr_t>(rows - 1) * ld + V) * esize, p1 = p0 + static_cast<uintptr_t>(rows) * V * 4;
+  if (l0 < p1 && p0 < l1 && (l0 != p0 || dtype != MTP_F32 || ld != V)) return MTP_ERR_INVALID_ARG;
 
   a.logits = logits;
   a.ld = ld;

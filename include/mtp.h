@@ -304,7 +304,7 @@ typedef struct mtp_logits_params {
  *   lowest index of the maximum.
  * Masked logits may hold anything; an allowed -inf is a probability of 0.
  *   logits: R * L rows of V elements (dtype MTP_F32 or MTP_BF16), ld elements
- *   apart (ld >= V); p [R, L, V] float (p may be the logits' own buffer when
+ *   apart (V <= ld <= 2^33); p [R, L, V] float (p may be the logits' own buffer when
  *   dtype is MTP_F32 and ld == V, and must not overlap them otherwise);
  *   status [R, L] int32 nullable = MTP_LOGITS_*; a row that is not OK is zero,
  *   which spec_verify reports as MTP_VERIFY_ZERO_RESIDUAL where it draws from

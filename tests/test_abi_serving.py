@@ -111,3 +111,17 @@ def test_draft_round_ext_host_validation(lib):
     size = lambda g, p: lib.mtp_draft_round_ext_workspace_bytes(ctypes.byref(dims), g, p)  # noqa: E731
     assert size(2, 0) == lib.mtp_draft_round_workspace_bytes(ctypes.byref(dims), 2) and size(2, 500) > size(2, 0)
     assert size(0, 0) == 0 and size(32, 0) == 0 and size(1, -1) == 0
+
+
+def test_logits_probs_refuses_overlapping_rows(lib):
+    from deepseek_sequential_mtp_gb300 import lib as binding
+
+    def call(logits, p, dtype=0, ld=100):
+        return lib.mtp_logits_probs(2, 3, 100, dtype, ctypes.c_void_p(logits), ld, ctypes.byref(binding.LogitsParams()),
+                                    ctypes.c_void_p(p), None, None)
+
+    at, p_bytes = 1 << 20, 6 * 100 * 4
+    assert call(at, at + 400) == 1 and call(at, at - 400) == 1      # a row on, a row back
+    assert call(at, at + 4 * (5 * 128 + 99), ld=128) == 1           # the last value of the last row
+    assert call(at, at - p_bytes + 4, dtype=1) == 1
+    assert call(at, at + 600, dtype=1) == 1                         # within the bf16 rows
