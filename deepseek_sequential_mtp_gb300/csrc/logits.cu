@@ -17,8 +17,9 @@
 // writes p.  Holding the slices in registers instead reads nothing twice but
 // leaves two CTAs per SM that wait for one phase after the other (120 us on
 // 320 rows of 129280 bf16 logits with a 2048-token history, mask and biases;
-// this form 76 us, 3.4 TB/s, and 59 us without penalties; a streaming copy of
-// the same bytes 41 us).  What is left is the latency of the marking's phases.
+// this form 74 us, 3.4 TB/s; of that the mask alone 59 us, a plain softmax 54, a
+// streaming copy of the same bytes 41).  What is left is the marking's phases, in
+// which every CTA of a cluster goes through the whole history.
 //
 // Penalties and biases are sparse, the row is dense.  A bit per vocabulary
 // entry of the slice marks the ids that occur; the ranks of the set bits
@@ -31,6 +32,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -40,7 +42,7 @@ namespace {
 
 // 256 threads with four vectors in flight, five CTAs per SM: over (threads,
 // vectors, CTAs per SM) = (512, 8, 2), (512, 4, 3), (1024, 2, 2) this one was
-// fastest on 320 rows of 129280 (76 us; 78, 80, 84) and within 2 us on few rows.
+// fastest on 320 rows of 129280 (by 2, 4 and 8 us) and within 2 us on few rows.
 constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 5;
 constexpr int kWarps = kThreads / 32;
@@ -126,11 +128,12 @@ logits_probs_kernel(const Args a) {
   const uint32_t* mask = q.mask ? q.mask + row * ((a.V + 31) / 32) + lo / 32 : nullptr;
   using Raw = typename std::conditional<VEC, Raw4<T>, float4>::type;
   Raw raw[kBatch];
-  auto fetch = [&](int b) {
+  // `whole`: no entry of the batch is past the end
+  auto fetch = [&](int b, auto whole) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       if constexpr (VEC) {  // n is a multiple of 4
-        if (off(b, i, 0) < n) raw[i] = *reinterpret_cast<const Raw*>(src + off(b, i, 0));
+        if (whole.value || off(b, i, 0) < n) raw[i] = *reinterpret_cast<const Raw*>(src + off(b, i, 0));
       } else {
         raw[i].x = off(b, i, 0) < n ? mtp::load_f32<T>(src + off(b, i, 0)) : -INFINITY;
         raw[i].y = off(b, i, 1) < n ? mtp::load_f32<T>(src + off(b, i, 1)) : -INFINITY;
@@ -140,15 +143,24 @@ logits_probs_kernel(const Args a) {
     }
   };
   // the live values of vector i, -inf for the others
-  auto values = [&](int b, int i, float (&z)[4]) {
+  auto values = [&](int b, int i, float (&z)[4], auto whole) {
     if constexpr (VEC) {
       const int o = off(b, i, 0);
       raw[i].get(z);
-      uint32_t on = o < n ? 0xFu : 0u;
-      if (a.live && o < n) on = live[o >> 5] >> (o & 31);
+      if (whole.value) {
+        if (a.live) {
+          const uint32_t on = live[o >> 5] >> (4 * t & 31);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (!((on >> e) & 1u)) z[e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (!(on & (1u << e))) z[e] = -INFINITY;
+        }
+      } else {
+        uint32_t on = o < n ? 0xFu : 0u;
+        if (a.live && o < n) on = live[o >> 5] >> (o & 31);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!(on & (1u << e))) z[e] = -INFINITY;
+      }
     } else {
       z[0] = raw[i].x; z[1] = raw[i].y; z[2] = raw[i].z; z[3] = raw[i].w;
       if (a.live) {
@@ -161,7 +173,14 @@ logits_probs_kernel(const Args a) {
     }
   };
   const int batches = (n + kBatchValues - 1) / kBatchValues;
-  fetch(0);
+  // runs f(b, whole) on batch b, with a form of its own for the whole ones
+  auto batch = [&](int b, auto f) {
+    if (VEC && (b + 1) * kBatchValues <= n)
+      f(std::true_type());
+    else
+      f(std::false_type());
+  };
+  fetch(0, std::false_type());
 
   const float temp = q.temperature ? q.temperature[r] : 1.f;
   const float rep = q.repetition ? q.repetition[r] : 1.f;
@@ -207,9 +226,20 @@ logits_probs_kernel(const Args a) {
     for (int i = t; i < nw; i += kThreads) marks[i] = 0u;
     for (int i = t; i < a.slots; i += kThreads) word[i] = 0u;
     __syncthreads();
-    for (int i = t; i < len; i += kThreads) mark(h[i]);
-    for (int i = t; i < n_draft; i += kThreads) mark(y[i]);
-    for (int i = t; i < q.n_bias; i += kThreads) mark(ids[i]);
+    // f(id, place) for a list's ids, four loads in flight per thread (one after the other they
+    // took a third of the marking's time)
+    auto each = [&](const int32_t* list, int count, auto f) {
+      for (int i = t; i < count; i += 4 * kThreads) {
+        int id[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) id[u] = i + u * kThreads < count ? list[i + u * kThreads] : -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) f(id[u], i + u * kThreads);
+      }
+    };
+    each(h, len, [&](int id, int) { mark(id); });
+    each(y, n_draft, [&](int id, int) { mark(id); });
+    each(ids, q.n_bias, [&](int id, int) { mark(id); });
     __syncthreads();
     {  // ranks: every thread counts a run of words, scanned over the CTA
       const int per = (nw + kThreads - 1) / kThreads, w0 = t * per;
@@ -242,14 +272,14 @@ logits_probs_kernel(const Args a) {
     __syncthreads();
     auto slot = [&](int v) { return before[v >> 5] + __popc(marks[v >> 5] & ((1u << (v & 31)) - 1u)); };
     if (q.n_bias > 0) {  // before the counts: a maximum over whole words
-      for (int i = t; i < q.n_bias; i += kThreads) {
-        const int v = entry(ids[i]);
+      each(ids, q.n_bias, [&](int id, int i) {
+        const int v = entry(id);
         if (v >= 0) {
           const uint32_t s = slot(v);
           token[s] = v;
           atomicMax(&word[s], static_cast<uint32_t>(i + 1) << kBiasShift);
         }
-      }
+      });
       __syncthreads();
     }
     auto count = [&](int id, uint32_t made_here) {
@@ -261,8 +291,8 @@ logits_probs_kernel(const Args a) {
         else atomicOr(&word[s], kSeenBit);
       }
     };
-    for (int i = t; i < len; i += kThreads) count(h[i], i >= made);
-    for (int i = t; i < n_draft; i += kThreads) count(y[i], 1u);
+    each(h, len, [&](int id, int i) { count(id, i >= made); });
+    each(y, n_draft, [&](int id, int) { count(id, 1u); });
   } else if (a.live) {
     for (int i = t; i * 32 < n; i += kThreads) live[i] = mask[i];
     __syncthreads();
@@ -270,35 +300,37 @@ logits_probs_kernel(const Args a) {
 
   // pass 1: maximum and sum
   for (int b = 0; b < batches; ++b) {
-    if (b > 0) fetch(b);
-    if (!greedy) {
-      float z[kBatch][4], mb = -INFINITY;
+    batch(b, [&](auto whole) {
+      if (b > 0) fetch(b, whole);
+      if (!greedy) {
+        float z[kBatch][4], mb = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        values(b, i, z[i]);
-        mb = fmaxf(mb, fmaxf(fmaxf(z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3])));  // passes over a NaN
+        for (int i = 0; i < kBatch; ++i) {
+          values(b, i, z[i], whole);
+          mb = fmaxf(mb, fmaxf(fmaxf(z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3])));  // passes over a NaN
+        }
+        // A NaN makes the sum NaN, and so does +inf (inf - inf).  (z k - m k
+        // would save an instruction, but overflows for logits at the type's
+        // lowest value and for small T.)
+        const float mn = fmaxf(mine.m, mb), mz = mn == -INFINITY ? 0.f : mn;
+        float s4[4] = {mine.s * ex2((mine.m - mz) * k), 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s4[e] += ex2((z[i][e] - mz) * k);
+        mine.s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        mine.m = mn;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          float z[4];
+          values(b, i, z, whole);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (off(b, i, e) < n) add(z[e], lo + off(b, i, e));
+        }
       }
-      // A NaN makes the sum NaN, and so does +inf (inf - inf).  (z k - m k
-      // would save an instruction, but overflows for logits at the type's
-      // lowest value and for small T.)
-      const float mn = fmaxf(mine.m, mb), mz = mn == -INFINITY ? 0.f : mn;
-      float s4[4] = {mine.s * ex2((mine.m - mz) * k), 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s4[e] += ex2((z[i][e] - mz) * k);
-      mine.s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-      mine.m = mn;
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        float z[4];
-        values(b, i, z);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (off(b, i, e) < n) add(z[e], lo + off(b, i, e));
-      }
-    }
+    });
   }
   if (a.sparse) {  // the marked ids, each step rounded once
     __syncthreads();
@@ -346,26 +378,29 @@ logits_probs_kernel(const Args a) {
   const float M = all.m, scale = greedy ? 1.f : 1.f / all.s;
   float* dst = a.p + row * a.V + lo;
   for (int b = 0; b < batches; ++b) {
-    if (batches > 1) fetch(b);
+    batch(b, [&](auto whole) {
+      if (batches > 1) fetch(b, whole);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      float z[4];
-      if (row_ok && !greedy) {
-        values(b, i, z);
+      for (int i = 0; i < kBatch; ++i) {
+        float z[4];
+        if (row_ok && !greedy) {
+          values(b, i, z, whole);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = ex2((z[e] - M) * k) * scale;
-      } else {
+          for (int e = 0; e < 4; ++e) z[e] = ex2((z[e] - M) * k) * scale;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = row_ok && lo + off(b, i, e) == all.best ? 1.f : 0.f;
+          for (int e = 0; e < 4; ++e) z[e] = row_ok && lo + off(b, i, e) == all.best ? 1.f : 0.f;
+        }
+        if constexpr (VEC) {
+          if (whole.value || off(b, i, 0) < n)
+            *reinterpret_cast<float4*>(dst + off(b, i, 0)) = make_float4(z[0], z[1], z[2], z[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (off(b, i, e) < n) dst[off(b, i, e)] = z[e];
+        }
       }
-      if constexpr (VEC) {
-        if (off(b, i, 0) < n) *reinterpret_cast<float4*>(dst + off(b, i, 0)) = make_float4(z[0], z[1], z[2], z[3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (off(b, i, e) < n) dst[off(b, i, e)] = z[e];
-      }
-    }
+    });
   }
   if (a.sparse && row_ok && !greedy) {  // over the zeros that the pass wrote for the marked ids
     __syncthreads();
