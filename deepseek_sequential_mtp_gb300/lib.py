@@ -185,15 +185,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-# the current stream's handle without the object around it (3 us of a small call), where torch has it
+# the current stream's handle without the object around it (3 us of a small call), and the
+# current device's number without the check for a first use, where torch has them
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream=None):
     if stream is None and _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+        return _raw_stream(_current_device())
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype):
@@ -220,7 +221,7 @@ def _arg(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, shape, device
 def _launch_device(t: torch.Tensor, stream):
     """The device of a call's tensors; it has to be the current one, and the stream's."""
     dev = t.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device() or (
+    if dev.type != "cuda" or dev.index != _current_device() or (
             stream is not None and stream.device != dev):
         raise MtpError(f"the tensors are on {dev}: make it the current device and use a stream of it")
     return dev
