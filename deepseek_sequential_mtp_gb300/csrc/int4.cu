@@ -47,9 +47,11 @@ constexpr int kMaxTokens = 32;
 
 // Variants by the number of 8-token tiles NT: with more than one, one CTA of 16
 // warps per SM shares the staged activations (16 tokens, 18432 x 7168: 28 us;
-// two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47).  With one, the
-// fixed part of a step weighs more: two CTAs of 8 warps and 256 weights of a row
-// per step (one token, 73728 x 7168: 62 us; three CTAs and 128 weights 72).
+// two CTAs of 8 warps 35; 32 tokens, 7168 x 18432: 43 and 47; 24 tokens on three
+// tiles 37, on four 41; 32 rows per warp, which read the activations half as often,
+// on 8 warps 47).  With one, the fixed part of a step weighs more: two CTAs of 8
+// warps and 256 weights of a row per step (one token, 73728 x 7168: 62 us; three
+// CTAs and 128 weights 72).
 template <int NT> struct Cfg {
   static constexpr int kChunk = NT > 1 ? 128 : 256;       // weights of a row per step
   static constexpr int kUnitBytes = 2 * kChunk;           // a token's activations of one chunk
@@ -478,7 +480,8 @@ mtp_status int4w_gemm_launch(const Int4Seg* segs, int nseg, int K, int group, co
   a.x = x;
   for (int i = 0; i < nseg; ++i)
     if (segs[i].n < 1) return MTP_ERR_SHAPE;
-  return R <= 8 ? plan<1>(a, segs, group, st) : R <= 16 ? plan<2>(a, segs, group, st) : plan<4>(a, segs, group, st);
+  return R <= 8 ? plan<1>(a, segs, group, st) : R <= 16 ? plan<2>(a, segs, group, st)
+         : R <= 24 ? plan<3>(a, segs, group, st) : plan<4>(a, segs, group, st);
 }
 
 }  // namespace mtp
