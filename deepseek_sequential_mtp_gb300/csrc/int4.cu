@@ -2,8 +2,9 @@
 //
 // Bound: HBM, half a byte per weight; what has to keep up with it is the
 // unpacking.  18432 x 7168, groups of 128: one token 21 us (3.4 TB/s), 8 tokens 27,
-// 32 tokens 43 (bound by the tokens' share of the work: mma.sync at its rate alone
-// takes 15); 73728 x 7168, one token 62 us (4.6 TB/s).  The products run on mma.sync.m16n8k16 with 16 weight rows as the
+// 16 29, 24 37, 32 42 (the tokens' share of the work, 7 us per 8: mma.sync alone
+// takes 4 of them, the reads of their fragments 3.5); 73728 x 7168, one token 62 us
+// (4.6 TB/s).  The products run on mma.sync.m16n8k16 with 16 weight rows as the
 // A operand and 8 tokens as B: (q - zero) is an integer of at most 5 bits, so
 // it is exact in bf16, the products with bf16 activations are exact in fp32
 // and a group's sum is multiplied by its scale in fp32 -- nothing is rounded

@@ -112,3 +112,15 @@ def test_refusals():
                      ((x[:, :248].contiguous(), q[:, :124].contiguous(), s, z), {}), ((x.t(), q, s, z), {})):
         with pytest.raises(lib.MtpError):
             lib.gemm_int4w(*args, **kw)
+
+
+@pytest.mark.parametrize("R", [18, 23, 24, 25])
+def test_tiles_of_tokens(R):
+    """Token counts around the borders of the tiles of 8, long enough for a split of k."""
+    for group, N, K in ((128, 700, 7168), (32, 130, 2080)):
+        x, q, s, z = _case(R, N, K, group, R % 2 == 0, 50 * R + group)
+        out = lib.gemm_int4w(*_dev(x, q, s, z), group=group)
+        torch.cuda.synchronize()
+        xd = x.double().numpy()
+        W = oi.dequantize(q.numpy(), s.double().numpy(), None if z is None else z.numpy(), group)
+        assert (np.abs(out.cpu().double().numpy() - xd @ W.T) <= _bound(xd, W, group) + 1e-30).all()
