@@ -42,9 +42,12 @@ namespace {
 
 // 256 threads with four vectors in flight, five CTAs per SM: over (threads,
 // vectors, CTAs per SM) = (512, 8, 2), (512, 4, 3), (1024, 2, 2) this one was
-// fastest on 320 rows of 129280 (by 2, 4 and 8 us) and within 2 us on few rows.
+// fastest on 320 rows of 129280 (by 2, 4 and 8 us).  Where the SMs hold the call's
+// CTAs three at a time, the form with room for the registers that five leave in
+// memory: one row of 32000 11.5 us instead of 16.5 in a graph, 28 rows 17.5 instead of
+// 19.6, 32 rows of 129280 21.6 instead of 23.6; 320 rows 81 instead of 73.
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 5;
+constexpr int kManyCtas = 5, kFewCtas = 3;  // per SM
 constexpr int kWarps = kThreads / 32;
 constexpr int kBatch = 4;                 // 4-value vectors a thread has in flight
 constexpr int kBatchValues = kBatch * 4 * kThreads;
@@ -96,8 +99,8 @@ template <> struct Raw4<__nv_bfloat16> {
 // Vector i of batch b of a thread holds the slice's entries off(b, i, 0..3):
 // with VEC four neighbours (16-byte accesses), else entries kThreads apart
 // (rows that are not 16-byte aligned).
-template <bool VEC, typename T>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <bool VEC, typename T, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas)
 logits_probs_kernel(const Args a) {
   extern __shared__ __align__(16) uint32_t smem[];
   __shared__ Part warp_part[kWarps];
@@ -417,10 +420,10 @@ constexpr int kMaxSmem = 200 * 1024;
 
 int smem_bytes(const Args& a) { return a.live ? 4 * (a.slice / 32) * (a.sparse ? 3 : 1) + 8 * a.slots : 0; }
 
-template <bool VEC, typename T>
-mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
+template <bool VEC, typename T, int kCtas>
+mtp_status launch_as(const Args& a, long long rows, int C, cudaStream_t st) {
   static mtp::PerDevice attr_smem, attr_cluster;
-  auto kernel = logits_probs_kernel<VEC, T>;
+  auto kernel = logits_probs_kernel<VEC, T, kCtas>;
   if (!mtp::smem_limit(attr_smem, kernel, kMaxSmem)) return MTP_ERR_CUDA;
   const int dev = mtp::current_device();
   if (C > 8 && dev >= 0 && (dev >= mtp::kMaxDevices || !attr_cluster.v[dev].load(std::memory_order_acquire))) {
@@ -440,6 +443,12 @@ mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
   MTP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
   mtp::note_launch();
   return MTP_OK;
+}
+
+template <bool VEC, typename T>
+mtp_status launch(const Args& a, long long rows, int C, cudaStream_t st) {
+  return rows * C <= kFewCtas * mtp::sm_count_current() ? launch_as<VEC, T, kFewCtas>(a, rows, C, st)
+                                                        : launch_as<VEC, T, kManyCtas>(a, rows, C, st);
 }
 
 }  // namespace

@@ -237,3 +237,19 @@ def test_refusals():
         with pytest.raises(lib.MtpError):
             lib.logits_probs(bad)
     assert lib.logits_probs(torch.zeros(0, 1, 5, device="cuda"))["p"].shape == (0, 1, 5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,L,V", [(130, 4, 5000), (125, 5, 4099), (4, 128, 9000)])
+def test_more_rows_than_the_few_row_form_takes(dtype, R, L, V):
+    """More CTAs than three per SM: whole batches and a last one, 16-byte rows and
+    odd ones, greedy rows and rows in place among them."""
+    a = _inputs(R, L, V, dtype, 90, 7, True, R + V)
+    a["temperature"][::9] = 0.0
+    _check(a, _run(a))
+    if dtype == torch.float32:
+        d = {k: (v.cuda() if torch.is_tensor(v) else v) for k, v in a.items()}
+        want = lib.logits_probs(**d)
+        out = {"p": d["logits"], "status": torch.empty((R, L), dtype=torch.int32, device="cuda")}
+        got = lib.logits_probs(**d, out=out)
+        assert torch.equal(got["p"], want["p"]) and torch.equal(got["status"], want["status"])
