@@ -631,8 +631,9 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     auto ship = [&](uint8_t* box, int col0, int row0w) {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0 && col0 < P.N && row0w < P.M) {
-        tma_store_2d(&tmOut, col0, row0w, smem_u32(box));
+      if (lane == 0) {
+        if (col0 < P.N && row0w < P.M) tma_store_2d(&tmOut, col0, row0w, smem_u32(box));
+        // a group per box, stored or not: claim() counts on the last one's being the other box
         bulk_commit();
       }
       nb ^= 1;
