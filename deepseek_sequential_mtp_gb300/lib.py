@@ -807,10 +807,12 @@ def _strides(t: torch.Tensor, name: str):
 
 
 def _pair(k, v, name: str, dims: int, device):
-    """Keys and values of one shape and layout, the last dimension dense."""
+    """Strides (None: dense) of keys and values of one shape and layout, the last dimension dense."""
     for t in (k, v):
         if t.dim() != dims or t.dtype is not torch.bfloat16 or t.device != device:
             raise MtpError(f"{name}_k and {name}_v must be bfloat16 tensors of {dims} dimensions on {device}")
+    if k.shape == v.shape and k.is_contiguous() and v.is_contiguous():
+        return None
     strides = _strides(k, name + "_k")
     if k.shape != v.shape or strides != _strides(v, name + "_v"):
         raise MtpError(f"{name}_k and {name}_v must have the same shape and strides")
@@ -838,8 +840,10 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     d = PrefixDims(R, L, H, Hkv, hd, P, 0, int(causal), 0.0 if scale is None else float(scale))
     if scale is not None and not 0.0 < scale < 3e38:
         raise MtpError("scale must be positive and finite")
-    d.q_stride_r, d.q_stride_t, d.q_stride_h = _strides(q, "q")
-    d.prefix_stride_t, d.prefix_stride_h = prefix_strides
+    if not q.is_contiguous():
+        d.q_stride_r, d.q_stride_t, d.q_stride_h = _strides(q, "q")
+    if prefix_strides is not None:
+        d.prefix_stride_t, d.prefix_stride_h = prefix_strides
     if (kv_k is None) != (kv_v is None):
         raise MtpError("kv_k and kv_v come together")
     if kv_k is not None:
@@ -847,7 +851,8 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
         if kv_k.shape[0] != R or tuple(kv_k.shape[2:]) != (Hkv, hd):
             raise MtpError("kv_k must be [R, T, Hkv, hd]")
         d.T = kv_k.shape[1]
-        d.kv_stride_r, d.kv_stride_t, d.kv_stride_h = kv_strides
+        if kv_strides is not None:
+            d.kv_stride_r, d.kv_stride_t, d.kv_stride_h = kv_strides
     elif ctx_len is not None:
         raise MtpError("ctx_len needs kv_k and kv_v")
     ctx = _arg(ctx_len, "ctx_len", torch.int32, (R,), dev)
