@@ -8,9 +8,10 @@
 // A operand and 8 tokens as B: (q - zero) is an integer of at most 5 bits, so
 // it is exact in bf16, the products with bf16 activations are exact in fp32
 // and a group's sum is multiplied by its scale in fp32 -- nothing is rounded
-// to fewer than 32 bits.  (tcgen05 would want the unpacked weights in shared
-// memory or TMEM first: 4 bytes moved per byte read, for an MMA of which at
-// most 32 of 128 columns are tokens.  e4m3 operands, for which a code is its
+// to fewer than 32 bits.  (On tcgen05, with the
+// unpacked weights in shared memory as the N = 256 side, 32 tokens take 49 us
+// instead of 42: each block is written and read there at four times its bytes.
+// e4m3 operands, for which a code is its
 // own byte, unpack in 3 instructions a word instead of 11, but mma.sync
 // executes them on this machine as two bf16-rate products after 17 more
 // instructions: 93 us instead of 43 on 7168 x 18432 with 32 tokens.)
