@@ -10,7 +10,7 @@
 // head), the tensor cores once some 300 rows share a head's prefix.  Measured, call
 // after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
 // to 256 own keys 79 us (4.4 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
-// 65 us (4.1 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
+// 63 us (4.2 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
 // to 512 own keys 63 us (350 TFLOP/s).  Each further key of such a prefix costs its
 // bytes at 6.6 TB/s in the first case, at 5.4 in the second, and 900 TFLOP/s in the
 // third; the rest is three kernels' way to their first data, one after the other.
