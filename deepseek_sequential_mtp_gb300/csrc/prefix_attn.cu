@@ -9,9 +9,9 @@
 // Bound: HBM for few rows (the keys and values once: 4 hd bytes per key and
 // head), the tensor cores once some 300 rows share a head's prefix.  Measured, call
 // after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
-// to 256 own keys 79 us (4.4 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
+// to 256 own keys 77 us (4.5 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
 // 63 us (4.2 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
-// to 512 own keys 63 us (350 TFLOP/s).  Each further key of such a prefix costs its
+// to 512 own keys 66 us (336 TFLOP/s).  Each further key of such a prefix costs its
 // bytes at 6.6 TB/s in the first case, at 5.4 in the second, and 900 TFLOP/s in the
 // third; the rest is three kernels' way to their first data, one after the other.
 //
@@ -56,9 +56,11 @@
 // and takes the SMs as they become free.
 //
 // Keys past a request's ctx_len may hold anything: their scores are replaced, and
-// their V rows are cleared in shared memory (0 times NaN is NaN).  P is rounded to
-// bf16 for the second product (half a step, 2^-8 of each weight at most; over many
-// keys as much as the output's own rounding, 1.4 of it together); statistics, sums
+// their V rows are cleared in shared memory (0 times NaN is NaN).  P enters the second
+// product as two bf16 parts, as in the draft step's own attention: its upper 16 bits
+// (kept by the first part exactly) and the rest, rounded to bf16 (2^-15 of the weight
+// together).  With one part the output was off by 1.4 of its own rounding; the second
+// costs the tensor-bound case 66 us instead of 60, the others nothing.  Statistics, sums
 // and records are fp32.  Every wait is bounded.
 #include <cuda.h>
 
@@ -488,10 +490,12 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
         }
         tc_fence_after();
         const uint32_t v_at = sV + (due_g % C::kVStages) * C::kTileBytes;
-        auto product = [&](int k) {
+        auto product = [&](int k) {  // with both parts of P
           const uint32_t bv = v_at + (k >> 2) * (C::kChunks * 8192) + (k & 3) * 2048;
-          umma_bf16_ts_warp(tmem + C::kColO + HD * due_x, tmem + 128u * due_x + 8u * k, sdesc_mn_sw128(bv), idesc_o,
-                            (!due_first || k > 0) ? 1u : 0u);
+          const uint64_t v_desc = sdesc_mn_sw128(bv);
+          const uint32_t p_at = tmem + 128u * due_x + 32u * (k >> 1) + 8u * (k & 1);
+          umma_bf16_ts_warp(tmem + C::kColO + HD * due_x, p_at, v_desc, idesc_o, (!due_first || k > 0) ? 1u : 0u);
+          umma_bf16_ts_warp(tmem + C::kColO + HD * due_x, p_at + 16, v_desc, idesc_o, 1u);
         };
         if (due_keys == kKeys / 16) {
 #pragma unroll
@@ -569,44 +573,57 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         if (live_warp) {
-          float sc[128];
-          {
-            float (&lo)[64] = *reinterpret_cast<float (*)[64]>(&sc[0]);
-            float (&hi)[64] = *reinterpret_cast<float (*)[64]>(&sc[64]);
-            tmem_ld64(lane_base + colS, lo);
-            tmem_ld64(lane_base + colS + 64, hi);
+          // S is read twice, 32 keys at a time (held whole, its 128 registers and the loops' length
+          // cost 3 us in 63): for the maximum, and for P, whose parts go over the columns that
+          // have been read
+          auto scores = [&](int c, float (&v)[32]) {
+            tmem_ld32(lane_base + colS + 32 * c, v);
+            const int left = see - key0 - 32 * c;
+            if (left < 32) {  // keys the row sees only in part
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (e >= left) v[e] = -INFINITY;
+            }
+          };
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            scores(c, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], v[e]);
           }
-          if (see - key0 < kKeys) {  // keys the row sees only in part
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (key0 + e >= see) sc[e] = -INFINITY;
-          }
-          float mx8[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mx8[e] = sc[e];
-#pragma unroll
-          for (int e = 8; e < 128; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], sc[e]);
-          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]))) * scale_log2;
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * scale_log2;
           // a new running maximum only when the block's exceeds the stale one by 2^8
           const float m_new = mx > m + kStaleMaxLog2 ? mx : m;
           const bool rescale = m_new != m && m != -INFINITY;
           const float neg = m_new == -INFINITY ? 0.f : -m_new;
-          float rs8[8];
+          float rs4[4] = {};
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float v[32];
+            scores(c, v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rs8[e] = 0.f;
+            for (int e = 0; e < 32; ++e) {
+              v[e] = ex2(fmaf(v[e], scale_log2, neg));
+              rs4[e & 3] += v[e];
+            }
+            uint32_t high[16], low[16];
 #pragma unroll
-          for (int e = 0; e < 64; ++e) {  // P pairs packed in place: sc[e] holds keys 2e, 2e+1
-            const float a = ex2(fmaf(sc[2 * e], scale_log2, neg));
-            const float b = ex2(fmaf(sc[2 * e + 1], scale_log2, neg));
-            rs8[e & 7] += a + b;
-            sc[e] = __uint_as_float(pack2_bf16(a, b));
+            for (int e = 0; e < 16; ++e) {
+              const uint32_t a = __float_as_uint(v[2 * e]), b = __float_as_uint(v[2 * e + 1]);
+              high[e] = __byte_perm(a, b, 0x7632);
+              low[e] = pack2_bf16(v[2 * e] - __uint_as_float(a & 0xFFFF0000u), v[2 * e + 1] - __uint_as_float(b & 0xFFFF0000u));
+            }
+            tmem_st16_nowait(lane_base + colS + 32 * c, high);
+            tmem_st16_nowait(lane_base + colS + 32 * c + 16, low);
           }
+          tmem_wait_st();
           if (__any_sync(0xffffffffu, rescale)) {  // O holds this segment's earlier P V: wait for the last one
             if (!wwait(pv_done(x), (n - 1) & 1)) { ok = false; break; }
             tc_fence_after();
             const float alpha = rescale ? ex2(m - m_new) : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
               float o[32];
               tmem_ld32(lane_base + colO + 32 * c, o);
@@ -617,12 +634,7 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
             l *= alpha;
           }
           m = m_new;
-          l += ((rs8[0] + rs8[1]) + (rs8[2] + rs8[3])) + ((rs8[4] + rs8[5]) + (rs8[6] + rs8[7]));
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float (&p)[32] = *reinterpret_cast<float (*)[32]>(&sc[32 * c]);
-            tmem_st32(lane_base + colS + 32 * c, p);
-          }
+          l += (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
         }
         tc_fence_before();
         mbar_arrive1(p_full(x));
@@ -744,7 +756,7 @@ __device__ __forceinline__ void small_block(SmallRows<HD>& w, uint32_t k_at, uin
     mma_16816(sc[0], w.qa[k], f[0], f[1]);
     mma_16816(sc[1], w.qa[k], f[2], f[3]);
   }
-  uint32_t pa[4];
+  uint32_t pa[4], pl[4];  // P's two parts
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int see = left - w.hidden[e];  // of these keys
@@ -762,8 +774,12 @@ __device__ __forceinline__ void small_block(SmallRows<HD>& w, uint32_t k_at, uin
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = ex2(fmaf(v[i], scale_log2, neg));
     w.sum[e] = w.sum[e] * alpha + ((v[0] + v[1]) + (v[2] + v[3]));
-    pa[e] = pack2_bf16(v[0], v[1]);
-    pa[2 + e] = pack2_bf16(v[2], v[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      pa[e + 2 * i] = pack2_bf16(v[2 * i], v[2 * i + 1]);
+      const float2 f = unpack2_bf16(pa[e + 2 * i]);
+      pl[e + 2 * i] = pack2_bf16(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+    }
     if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
       for (int n = 0; n < HD / 8; ++n) {
@@ -778,6 +794,8 @@ __device__ __forceinline__ void small_block(SmallRows<HD>& w, uint32_t k_at, uin
     ldsm_x4_t(swz(v_at + (n >> 2) * kChunk, key + (lane & 15), 16 * (n & 3) + 8 * (lane >> 4)), f);
     mma_16816(w.o[2 * n], pa, f[0], f[1]);
     mma_16816(w.o[2 * n + 1], pa, f[2], f[3]);
+    mma_16816(w.o[2 * n], pl, f[0], f[1]);
+    mma_16816(w.o[2 * n + 1], pl, f[2], f[3]);
   }
 }
 enum : int { kFirst = 1, kLast = 2, kOwn = 4 };

@@ -448,7 +448,7 @@ size_t mtp_prefix_attention_workspace_bytes(const mtp_prefix_dims* dims);
  *   ws: mtp_prefix_attention_workspace_bytes(dims) bytes, 16-byte aligned; calls
  *   that may overlap need workspaces of their own.
  * Scores, softmax statistics and outputs are fp32; the softmax weights enter
- * the product with the values as bf16. */
+ * the product with the values as two bf16 parts (2^-15 of a weight). */
 mtp_status mtp_prefix_attention(const mtp_prefix_dims* dims, const void* q, const void* prefix_k, const void* prefix_v,
                                 const void* kv_k, const void* kv_v, const int32_t* ctx_len, void* out, float* lse,
                                 void* ws, size_t ws_bytes, cudaStream_t stream);
@@ -517,8 +517,8 @@ typedef struct mtp_block_int4 {
  *   prefix_k, prefix_v [prefix_len, d] bf16, 16-byte aligned: keys and values, as
  *   the cache holds them, of rows that precede every request's own cache (a
  *   prompt that the batch shares).  They are kept and read once for the batch;
- *   the result is that of caches which begin with these rows, to the rounding of
- *   the prefix's softmax weights to bf16.  pos may reach T + prefix_len. */
+ *   the result is that of caches which begin with these rows, to 2^-15 of the
+ *   prefix's softmax weights.  pos may reach T + prefix_len. */
 typedef struct mtp_draft_ext {
   const mtp_block_fp8* fp8;
   const mtp_block_int4* int4;
