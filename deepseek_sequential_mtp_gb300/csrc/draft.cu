@@ -663,6 +663,9 @@ softmax_sample_kernel(float* __restrict__ q, int V, size_t ldq, uint2 key, uint3
   __shared__ int s_cstar;
   __shared__ double s_before, s_target;
   cg::cluster_group cluster = cg::this_cluster();
+  // CTA 0's shared memory may be written once it has started: a CTA without a chunk (seven of
+  // them at V <= 1024) is at its store long before pass A ends elsewhere
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int rank = static_cast<int>(cluster.block_rank());
   const int r = blockIdx.x / kSampleCluster;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -689,6 +692,7 @@ softmax_sample_kernel(float* __restrict__ q, int V, size_t ldq, uint2 key, uint3
     merge_max_sum(m, sm, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sm, o));
   if (lane == 0) s_red[warp] = make_float2(m, sm);
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int w = 1; w < kSampleThreads / 32; ++w) merge_max_sum(m, sm, s_red[w].x, s_red[w].y);
     *cluster.map_shared_rank(&s_ms[rank], 0) = make_float2(m, sm);
