@@ -9,7 +9,7 @@
 // Bound: HBM for few rows (the keys and values once: 4 hd bytes per key and
 // head), the tensor cores once some 300 rows share a head's prefix.  Measured, call
 // after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
-// to 256 own keys 77 us (4.5 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
+// to 256 own keys 76 us (4.6 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
 // 63 us (4.2 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
 // to 512 own keys 66 us (336 TFLOP/s).  Each further key of such a prefix costs its
 // bytes at 6.6 TB/s in the first case, at 5.4 in the second, and 900 TFLOP/s in the
@@ -56,7 +56,8 @@
 // and takes the SMs as they become free.
 //
 // Keys past a request's ctx_len may hold anything: their scores are replaced, and
-// their V rows are cleared in shared memory (0 times NaN is NaN).  P enters the second
+// their V rows are cleared in shared memory (0 times NaN is NaN); rows of new tokens that
+// an earlier token does not see may as well (see_again below).  P enters the second
 // product as two bf16 parts, as in the draft step's own attention: its upper 16 bits
 // (kept by the first part exactly) and the rest, rounded to bf16 (2^-15 of the weight
 // together).  With one part the output was off by 1.4 of its own rounding; the second
@@ -946,10 +947,62 @@ constexpr int kJoinWarps = 4;
 // instead of 85, with 512 of 60 36 instead of 40; with 1792 of 12 111 instead of 108, with 5120 of
 // 20 85 instead of 75.
 constexpr int kSplitRows = 8;
+// what the join needs of the own caches where it takes them up itself (see_again)
+struct OwnRows {
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_r, q_l, q_h, k_r, k_t, k_h;
+  float scale_log2;
+};
+// kD consecutive bf16
+template <int kD>
+__device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&f)[kD]) {
+#pragma unroll
+  for (int d = 0; d < kD; d += 2) {
+    const float2 v = unpack2_bf16(*reinterpret_cast<const uint32_t*>(p + d));
+    f[d] = v.x;
+    f[d + 1] = v.y;
+  }
+}
+// The output of a row (request r, token i, head h) over the prefix's n0 records and the first
+// `see` rows of its own cache, one at a time, by a warp.  The products take 16 keys of all the
+// rows together, with a weight of 0 where a row does not see a key, and 0 times the NaN or the
+// infinity that a later token's value may hold (a padded draft's) is NaN.  The maxima and
+// sums are free of it; where an output is not finite, it is worked out again from what it sees.
+template <int kD>
+__device__ __forceinline__ void see_again(float (&acc)[kD], const OwnRows& own, const float2* rec_ml, const float* rec_o,
+                                       long long at0, int step0, int n0, int r, int i, int h, int head, int see, float M,
+                                       int lane) {
+#pragma unroll
+  for (int d = 0; d < kD; ++d) acc[d] = 0.f;
+#pragma unroll 1
+  for (int p = 0; p < n0; ++p) {
+    const long long at = at0 + static_cast<long long>(p) * step0;
+    const float2 ml = rec_ml[at];
+    if (!(ml.y > 0.f)) continue;
+    const float w = ex2(ml.x - M);
+#pragma unroll
+    for (int d = 0; d < kD; ++d) acc[d] = fmaf(w, rec_o[at * (32 * kD) + lane * kD + d], acc[d]);
+  }
+  float q[kD];
+  load_bf16<kD>(own.q + r * own.q_r + i * own.q_l + h * own.q_h + lane * kD, q);
+  const long long at = r * own.k_r + head * own.k_h + lane * kD;
+#pragma unroll 1
+  for (int j = 0; j < see; ++j) {
+    float k[kD], v[kD], s = 0.f;
+    load_bf16<kD>(own.k + at + j * own.k_t, k);
+    load_bf16<kD>(own.v + at + j * own.k_t, v);
+#pragma unroll
+    for (int d = 0; d < kD; ++d) s = fmaf(q[d], k[d], s);
+    const float w = ex2(fmaf(warp_sum(s), own.scale_log2, -M));
+#pragma unroll
+    for (int d = 0; d < kD; ++d) acc[d] = fmaf(w, v[d], acc[d]);
+  }
+}
+
 template <int HD, int kSplit>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const float* __restrict__ rec_o,
-                   __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
+prefix_join_kernel(const Shape sh, const __grid_constant__ OwnRows own, const float2* __restrict__ rec_ml,
+                   const float* __restrict__ rec_o, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   static_assert(kSplit == 1 || kSplit == kJoinWarps, "a row per warp, or per CTA");
   const int r = blockIdx.y, item = kSplit > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
@@ -1072,6 +1125,13 @@ prefix_join_kernel(const Shape sh, const float2* __restrict__ rec_ml, const floa
       for (int d = 0; d < kD; ++d) acc[d] += f * s_o[w][lane * kD + d];
     }
   }
+  if (sh.causal && nb > 0 && i + 1 < sh.L) {  // rows of later tokens stand beside this one's
+    bool odd = false;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) odd |= !(fabsf(acc[d]) < INFINITY);
+    if (__any_sync(0xffffffffu, odd) && L == L)
+      see_again<kD>(acc, own, rec_ml, rec_o, at0, step0, n0, r, i, h, head, max(0, sh.ctx(r) - sh.L + 1 + i), M, lane);
+  }
   const long long out = (static_cast<long long>(r) * sh.L + i) * sh.H + h;
   if (rec) {
     float* to = rec + out * rec_stride;
@@ -1190,10 +1250,11 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   const bool split = static_cast<long long>(s.R) * s.L * s.H <= kSplitRows * sm_count_current();
   const dim3 grid(split ? s.L * s.H : (s.L * s.H + kJoinWarps - 1) / kJoinWarps, s.R);
   auto join = split ? prefix_join_kernel<HD, kJoinWarps> : prefix_join_kernel<HD, 1>;
+  const OwnRows own{p.q, p.kk, p.kv, p.q_r, p.q_l, p.q_h, p.k_r, p.k_t, p.k_h, scale_log2};
   if (p.P > 0 || p.T > 0)
-    MTP_CUDA_TRY(launch_pdl(join, grid, dim3(32 * kJoinWarps), 0, st, s, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
+    MTP_CUDA_TRY(launch_pdl(join, grid, dim3(32 * kJoinWarps), 0, st, s, own, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
   else
-    join<<<grid, 32 * kJoinWarps, 0, st>>>(s, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
+    join<<<grid, 32 * kJoinWarps, 0, st>>>(s, own, ml, ro, p.o, p.lse, p.rec, p.rec_stride);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;

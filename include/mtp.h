@@ -439,8 +439,8 @@ size_t mtp_prefix_attention_workspace_bytes(const mtp_prefix_dims* dims);
  *   j < ctx_len[r] - (L - 1 - i)   if causal (the last L rows are the new
  *                                  tokens' own: each sees itself and what precedes it),
  *   j < ctx_len[r]                 otherwise.
- * The cache rows from ctx_len[r] on are not used and may hold anything.  Keys
- * are used as stored.  A token that sees no row gets zeros (and lse = -inf).
+ * Rows that a token does not see (from ctx_len[r] on; of later tokens) may hold
+ * anything, padding and NaN among it.  Keys are used as stored.  A token that sees no row gets zeros (and lse = -inf).
  *   q, prefix_k, prefix_v, kv_k, kv_v: bf16, 16-byte aligned; ctx_len [R]
  *   int32, nullable (T), clamped to [0, T]; out [R, L, n_heads, head_dim] bf16;
  *   lse [R, L, n_heads] float, nullable: the natural logarithm of the softmax's
