@@ -122,7 +122,7 @@ logits_probs_kernel(const Args a) {
   uint32_t* marks = live + nw;    // [nw] ids that occur, or have a bias
   uint32_t* before = marks + nw;  // [nw] marked ids in the words before
   uint32_t* word = before + nw;   // [slots] what happens to a marked id, later its z
-  int* token = reinterpret_cast<int*>(word + a.slots);  // [slots] its entry of the slice
+  uint16_t* token = reinterpret_cast<uint16_t*>(word + a.slots);  // [slots] its entry of the slice
 
   auto off = [&](int b, int i, int e) {
     return b * kBatchValues + (VEC ? (i * kThreads + t) * 4 + e : (i * 4 + e) * kThreads + t);
@@ -279,7 +279,7 @@ logits_probs_kernel(const Args a) {
         const int v = entry(id);
         if (v >= 0) {
           const uint32_t s = slot(v);
-          token[s] = v;
+          token[s] = static_cast<uint16_t>(v);
           atomicMax(&word[s], static_cast<uint32_t>(i + 1) << kBiasShift);
         }
       });
@@ -289,7 +289,7 @@ logits_probs_kernel(const Args a) {
       const int v = entry(id);
       if (v >= 0) {
         const uint32_t s = slot(v);
-        token[s] = v;
+        token[s] = static_cast<uint16_t>(v);
         if (made_here) atomicAdd(&word[s], 1u);
         else atomicOr(&word[s], kSeenBit);
       }
@@ -416,9 +416,15 @@ logits_probs_kernel(const Args a) {
                                          : MTP_LOGITS_OK;
 }
 
-constexpr int kMaxSmem = 200 * 1024;
+// What the largest slice needs with all of its entries marked: no call is beyond it, whatever
+// the sizes allowed below.
+constexpr int kMaxSlice = kMaxVocab / kMaxCluster;
+static_assert(kMaxSlice == kTargetSlice && kMaxSlice <= 65536, "a slice's entries are 16-bit numbers");
+constexpr int smem_for(int slice, int slots, bool sparse) { return 4 * (slice / 32) * (sparse ? 3 : 1) + 6 * slots; }
+constexpr int kMaxSmem = smem_for(kMaxSlice, kMaxSlice, true);
+static_assert(kMaxSmem <= 226 * 1024, "beside the static arrays");
 
-int smem_bytes(const Args& a) { return a.live ? 4 * (a.slice / 32) * (a.sparse ? 3 : 1) + 8 * a.slots : 0; }
+int smem_bytes(const Args& a) { return a.live ? smem_for(a.slice, a.slots, a.sparse) : 0; }
 
 template <bool VEC, typename T, int kCtas>
 mtp_status launch_as(const Args& a, long long rows, int C, cudaStream_t st) {
