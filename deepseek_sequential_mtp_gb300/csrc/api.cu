@@ -80,7 +80,7 @@ extern "C" const char* mtp_status_string(int s) {
 extern "C" int mtp_abi_version(void) { return MTP_ABI_VERSION; }
 
 extern "C" mtp_status mtp_check_errors(cudaStream_t stream, unsigned int* flags) {
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return MTP_ERR_CUDA;
+  MTP_CUDA_TRY(cudaStreamSynchronize(stream));
   const unsigned int parts[8] = {mtp_take_errors_chain(), mtp_take_errors_gemm(), mtp_take_errors_attn(),
                                  mtp_take_errors_verify(), mtp_take_errors_draft(), mtp_take_errors_fp8(),
                                  mtp_take_errors_dgemm(), mtp_take_errors_prefix()};

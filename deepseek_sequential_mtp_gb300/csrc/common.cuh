@@ -10,10 +10,16 @@
 
 #include "../../include/mtp.h"
 
+// A failed runtime call also leaves its error for the thread's next launch check, which would
+// report it for a launch of its own: every failure is taken back where it is returned.
+inline bool mtp_cuda_ok(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e == cudaSuccess;
+}
+
 #define MTP_CUDA_TRY(expr)                                \
   do {                                                    \
-    cudaError_t mtp_e_ = (expr);                          \
-    if (mtp_e_ != cudaSuccess) return MTP_ERR_CUDA;       \
+    if (!mtp_cuda_ok(expr)) return MTP_ERR_CUDA;          \
   } while (0)
 
 #define MTP_LAUNCH_CHECK()                                \
@@ -30,9 +36,9 @@
   static __device__ unsigned int g_mtp_error_word = 0;                        \
   unsigned int take_fn() {                                                    \
     unsigned int v = 0, zero = 0;                                             \
-    if (cudaMemcpyFromSymbol(&v, g_mtp_error_word, sizeof(v)) != cudaSuccess) \
+    if (!mtp_cuda_ok(cudaMemcpyFromSymbol(&v, g_mtp_error_word, sizeof(v))))  \
       return 0xFFFFFFFFu;                                                     \
-    cudaMemcpyToSymbol(g_mtp_error_word, &zero, sizeof(zero));                \
+    mtp_cuda_ok(cudaMemcpyToSymbol(g_mtp_error_word, &zero, sizeof(zero)));   \
     return v;                                                                 \
   }
 
@@ -56,7 +62,7 @@ struct PerDevice {
 };
 inline int current_device() {
   int d = -1;
-  return cudaGetDevice(&d) == cudaSuccess ? d : -1;
+  return mtp_cuda_ok(cudaGetDevice(&d)) ? d : -1;
 }
 // Raise `kernel`'s dynamic shared-memory limit to `bytes` on the current
 // device, once per device.
@@ -65,7 +71,7 @@ inline bool smem_limit(PerDevice& done, Kernel* kernel, int bytes) {
   const int dev = current_device();
   if (dev < 0) return false;
   if (dev < kMaxDevices && done.v[dev].load(std::memory_order_acquire)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (!mtp_cuda_ok(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes))) return false;
   if (dev < kMaxDevices) done.v[dev].store(1, std::memory_order_release);
   return true;
 }
@@ -78,7 +84,7 @@ inline int sm_count_current() {
     if (c > 0) return c;
   }
   int n = 0;
-  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+  if (dev < 0 || !mtp_cuda_ok(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev)) || n <= 0) n = 148;
   if (dev >= 0 && dev < kMaxDevices) cache.v[dev].store(n, std::memory_order_relaxed);
   return n;
 }

@@ -30,7 +30,7 @@ void* g_scratch_ptr[mtp::kMaxDevices] = {};
 // Device address of the scratch array on the current device (looked up once).
 mtp_status scratch_for_current_device(void** out) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return MTP_ERR_CUDA;
+  MTP_CUDA_TRY(cudaGetDevice(&dev));
   if (dev < 0 || dev >= mtp::kMaxDevices) return MTP_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lock(g_setup_mutex);
   if (!g_scratch_ptr[dev]) {
