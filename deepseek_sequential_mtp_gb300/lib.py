@@ -414,10 +414,13 @@ class Fp8Block:
 
 class Int4Block:
     """ctypes view of the 4-bit linear maps of one module: int4[name] = (q, scale,
-    zero or None) as _int4_matrix takes them."""
+    zero or None) as _int4_matrix takes them, all on one GPU."""
 
     def __init__(self, int4: dict, group: int, cfg):
         d, f = cfg.d, cfg.ffn
+        device = int4[FP8_LINEAR_MAPS[0]][0].device
+        if device.type != "cuda":
+            raise MtpError("4-bit weights must be CUDA tensors")
         self.int4 = int4
         self.struct = BlockInt4()
         self.struct.group = int(group)
@@ -427,7 +430,7 @@ class Int4Block:
             n, k = shapes.get(name, (d, d))
             if tuple(q.shape) != (n, k // 2):
                 raise MtpError(f"{name}.q must be [{n}, {k // 2}]")
-            setattr(self.struct, name, _int4_matrix(name, q, sc, z, int(group), q.device))
+            setattr(self.struct, name, _int4_matrix(name, q, sc, z, int(group), device))
 
 
 def gemm_decode_bf16(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, stream=None):
@@ -864,8 +867,11 @@ def prefix_attention(q: torch.Tensor, prefix_k: torch.Tensor, prefix_v: torch.Te
     lib = load()
     if ws is None:
         ws = _empty(int(lib.mtp_prefix_attention_workspace_bytes(ctypes.byref(d))), torch.uint8, dev, stream)
+    elif ws.device != dev or not ws.is_contiguous():
+        raise MtpError(f"ws must be a contiguous tensor on {dev}")
     st = lib.mtp_prefix_attention(ctypes.byref(d), q.data_ptr(), prefix_k.data_ptr(), prefix_v.data_ptr(),
                                   kv_k.data_ptr() if d.T > 0 else None, kv_v.data_ptr() if d.T > 0 else None, ctx,
-                                  out["o"].data_ptr(), out["lse"].data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                                  out["o"].data_ptr(), out["lse"].data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                  _stream(stream))
     _check(st, "mtp_prefix_attention")
     return out
