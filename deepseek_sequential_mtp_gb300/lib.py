@@ -684,11 +684,12 @@ def kernel_launches() -> int:
 # --------------------------------------------------------------------------
 class _Draft:
     """Call state of a draft round of ``gamma`` steps for one shape: dims, weight
-    views, workspace."""
+    views, workspace.  ``rows`` is the outputs' leading shape."""
 
-    def __init__(self, cfg, weights: dict, gamma: int, device, fp8, int4, int4_group, prefix_len):
+    def __init__(self, cfg, weights: dict, gamma: int, rows: tuple, device, fp8, int4, int4_group, prefix_len):
         self.cfg = cfg
         self.gamma = int(gamma)
+        self.rows = rows
         self.prefix_len = int(prefix_len)
         self.dims = Dims(cfg.R, cfg.ctx, cfg.d, cfg.n_heads, cfg.head_dim, cfg.ffn, cfg.V, 1, cfg.eps,
                          cfg.rope_base, MTP_BF16)
@@ -703,15 +704,18 @@ class _Draft:
             raise MtpError("invalid draft-step dimensions or gamma")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
 
-    def run(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream, prefix_k, prefix_v):
+    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
+                 out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
         cfg, g = self.cfg, self.gamma
-        _need(parent_hidden, "parent_hidden", torch.bfloat16)
-        for name, t in (("kv_k", kv_k), ("kv_v", kv_v)):
-            _need(t, name, torch.bfloat16)
-            if tuple(t.shape) != (cfg.R, cfg.ctx, cfg.d):
-                raise MtpError(f"{name} must be [R, ctx, d]")
-        for name, t in (("frontier", frontier), ("pos", pos), ("ctx_len", ctx_len)):
-            _need(t, name, torch.int32)
+        dev = _launch_device(parent_hidden, stream)
+        if self.ws.device != dev:
+            raise MtpError(f"the draft step was built on {self.ws.device}, its inputs are on {dev}")
+        bf16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+        rows = [_arg(t, name, dtype, shape, dev) for t, name, dtype, shape in (
+            (parent_hidden, "parent_hidden", bf16, (cfg.R, cfg.d)), (frontier, "frontier", i32, (cfg.R,)),
+            (pos, "pos", i32, (cfg.R,)), (kv_k, "kv_k", bf16, (cfg.R, cfg.ctx, cfg.d)),
+            (kv_v, "kv_v", bf16, (cfg.R, cfg.ctx, cfg.d)), (ctx_len, "ctx_len", i32, (cfg.R,)))]
+        h = _arg(h_out, "h_out", bf16, (*self.rows, cfg.d), dev)
         ext = None
         if self.i4 is not None or self.prefix_len > 0:
             ext = DraftExt()
@@ -723,20 +727,25 @@ class _Draft:
                 for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)):
                     if t is None:
                         raise MtpError(f"{name} is missing")
-                    _arg(t, name, torch.bfloat16, (self.prefix_len, cfg.d), parent_hidden.device)
+                    _arg(t, name, bf16, (self.prefix_len, cfg.d), dev)
                 ext.prefix_k, ext.prefix_v, ext.prefix_len = prefix_k.data_ptr(), prefix_v.data_ptr(), self.prefix_len
         if self.prefix_len == 0 and (prefix_k is not None or prefix_v is not None):
             raise MtpError("prefix rows were given to a draft step built with prefix_len = 0")
-        rows = (_ptr(parent_hidden), _ptr(frontier), _ptr(pos), _ptr(kv_k), _ptr(kv_v), _ptr(ctx_len))
-        rest = (int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), _ptr(out["q"]), _ptr(out["y"]), _ptr(h_out),
-                _ptr(self.ws), self.ws.numel(), _stream(stream))
+        if out is None:
+            out = {"q": _empty((*self.rows, cfg.V), f32, dev, stream), "y": _empty(self.rows, i32, dev, stream)}
+        q = _arg(out["q"], "out['q']", f32, (*self.rows, cfg.V), dev)
+        y = _arg(out["y"], "out['y']", i32, self.rows, dev)
+        if stream is not None:
+            self.ws.record_stream(stream)  # allocated on another one
+        rest = (int(seed) & (2**64 - 1), int(offset) & (2**64 - 1), q, y, h, self.ws.data_ptr(), self.ws.numel(),
+                _stream(stream))
         dims, w = ctypes.byref(self.dims), ctypes.byref(self.w.struct)
         if ext is not None:
             _check(load().mtp_draft_round_ext(dims, w, ctypes.byref(ext), *rows, g, *rest), "mtp_draft_round_ext")
         elif self.f8 is not None:
             _check(load().mtp_draft_round_fp8(dims, w, ctypes.byref(self.f8.struct), *rows, g, *rest),
                    "mtp_draft_round_fp8")
-        elif isinstance(self, DraftStep):
+        elif len(self.rows) == 1:
             _check(load().mtp_draft_step(dims, w, *rows, *rest), "mtp_draft_step")
         else:
             _check(load().mtp_draft_round(dims, w, *rows, g, *rest), "mtp_draft_round")
@@ -750,45 +759,25 @@ class DraftStep(_Draft):
     The module's linear maps may be in FP8 (``fp8``) or in 4 bits (``int4``:
     name -> (q, scale, zero or None), groups of ``int4_group``), and the caches
     may begin with ``prefix_len`` rows that all requests share, passed to each
-    call as prefix_k and prefix_v [prefix_len, d] (mtp_draft_round_ext)."""
+    call as prefix_k and prefix_v [prefix_len, d] (mtp_draft_round_ext).  A call
+    takes parent_hidden [R, d], frontier, pos, ctx_len [R] and kv_k, kv_v [R, ctx, d]
+    on the step's device and returns {"q": [R, V] float32, "y": [R] int32} and,
+    where h_out [R, d] is given, "h"; ``out`` may supply them.  Calls of one object
+    share its workspace and must not overlap."""
 
     def __init__(self, cfg, weights: dict, device="cuda", fp8: Optional[dict] = None, int4: Optional[dict] = None,
                  int4_group: int = 128, prefix_len: int = 0):
-        super().__init__(cfg, weights, 1, device, fp8, int4, int4_group, prefix_len)
-
-    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
-                 out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
-        cfg = self.cfg
-        dev = parent_hidden.device
-        if out is None:
-            out = {"q": torch.empty((cfg.R, cfg.V), dtype=torch.float32, device=dev),
-                   "y": torch.empty(cfg.R, dtype=torch.int32, device=dev)}
-        return self.run(parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream,
-                        prefix_k, prefix_v)
+        super().__init__(cfg, weights, 1, (cfg.R,), device, fp8, int4, int4_group, prefix_len)
 
 
 class DraftRound(_Draft):
     """Reusable call state of mtp_draft_round: gamma recurrent draft steps of
-    one module for one shape (see synth.DraftConfig).  ``fp8``, ``int4`` and
-    ``prefix_len`` as for DraftStep."""
+    one module for one shape (see synth.DraftConfig).  As DraftStep, with outputs
+    [R, gamma, V], [R, gamma] and h_out [R, gamma, d]."""
 
     def __init__(self, cfg, weights: dict, gamma: int, device="cuda", fp8: Optional[dict] = None,
                  int4: Optional[dict] = None, int4_group: int = 128, prefix_len: int = 0):
-        super().__init__(cfg, weights, gamma, device, fp8, int4, int4_group, prefix_len)
-
-    def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
-                 out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
-        cfg, g = self.cfg, self.gamma
-        if h_out is not None:
-            _need(h_out, "h_out", torch.bfloat16)
-            if tuple(h_out.shape) != (cfg.R, g, cfg.d):
-                raise MtpError("h_out must be [R, gamma, d]")
-        dev = parent_hidden.device
-        if out is None:
-            out = {"q": torch.empty((cfg.R, g, cfg.V), dtype=torch.float32, device=dev),
-                   "y": torch.empty((cfg.R, g), dtype=torch.int32, device=dev)}
-        return self.run(parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset, out, h_out, stream,
-                        prefix_k, prefix_v)
+        super().__init__(cfg, weights, gamma, (cfg.R, int(gamma)), device, fp8, int4, int4_group, prefix_len)
 
 
 # --------------------------------------------------------------------------
