@@ -376,15 +376,18 @@ def make_dims(cfg) -> Dims:
 
 
 class ChainWeights:
-    """Holds the ctypes views of a weight dict (see synth.make_weights)."""
+    """Holds the ctypes views of a weight dict (see synth.make_weights); the lists
+    named in ``without`` are not read and may be missing."""
 
-    def __init__(self, weights: dict, D: int):
+    def __init__(self, weights: dict, D: int, without=()):
         self._keep = []
         self.struct = Weights()
         self.struct.embed = weights["embed"].data_ptr()
         self.struct.head = weights["head"].data_ptr()
         self.struct.out_norm = weights["out_norm"].data_ptr()
         for k in _WEIGHT_LISTS:
+            if k in without:
+                continue
             lst = weights[k]
             if len(lst) != D:
                 raise MtpError(f"weights[{k!r}] must have D={D} entries")
@@ -693,16 +696,28 @@ class _Draft:
         self.prefix_len = int(prefix_len)
         self.dims = Dims(cfg.R, cfg.ctx, cfg.d, cfg.n_heads, cfg.head_dim, cfg.ffn, cfg.V, 1, cfg.eps,
                          cfg.rope_base, MTP_BF16)
-        self.weights = weights
-        self.w = ChainWeights(weights, 1)
         if fp8 is not None and int4 is not None:
             raise MtpError("a module has its linear maps in FP8 or in 4 bits, not both")
+        # maps in another form replace the weight dict's, which are neither read nor kept
+        without = FP8_LINEAR_MAPS if fp8 is not None or int4 is not None else ()
+        self.weights = {k: v for k, v in weights.items() if k not in without}
+        d, f = cfg.d, cfg.ffn
+        shapes = {"embed": (cfg.V, d), "head": (cfg.V, d), "out_norm": (d,), "hnorm": (d,), "enorm": (d,),
+                  "attn_norm": (d,), "ffn_norm": (d,), "eh_proj": (d, 2 * d), "w_gate": (f, d), "w_up": (f, d),
+                  "w_down": (d, f)}
+        for name, t in self.weights.items():
+            for m in t if isinstance(t, (list, tuple)) else (t,):
+                _arg(m, f"weights[{name!r}]", torch.bfloat16, shapes.get(name, (d, d)), self.weights["embed"].device)
+        self.w = ChainWeights(self.weights, 1, without)
         self.f8 = Fp8Block(fp8) if fp8 is not None else None
         self.i4 = Int4Block(int4, int4_group, cfg) if int4 is not None else None
         nbytes = int(load().mtp_draft_round_ext_workspace_bytes(ctypes.byref(self.dims), self.gamma, self.prefix_len))
         if nbytes == 0:
             raise MtpError("invalid draft-step dimensions or gamma")
         self.ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        blocks = [b[FP8_LINEAR_MAPS[0]][0] for b in (fp8, int4) if b is not None]
+        if any(t.device != self.ws.device for t in (self.weights["embed"], *blocks)):
+            raise MtpError(f"the weights and the draft step ({self.ws.device}) must be on one device")
 
     def __call__(self, parent_hidden, frontier, pos, kv_k, kv_v, ctx_len, seed, offset,
                  out=None, h_out=None, stream=None, prefix_k=None, prefix_v=None):
@@ -757,7 +772,8 @@ class _Draft:
 class DraftStep(_Draft):
     """Reusable call state of mtp_draft_step for one shape (see synth.DraftConfig).
     The module's linear maps may be in FP8 (``fp8``) or in 4 bits (``int4``:
-    name -> (q, scale, zero or None), groups of ``int4_group``), and the caches
+    name -> (q, scale, zero or None), groups of ``int4_group``; ``weights`` need not
+    hold the bf16 maps then), and the caches
     may begin with ``prefix_len`` rows that all requests share, passed to each
     call as prefix_k and prefix_v [prefix_len, d] (mtp_draft_round_ext).  A call
     takes parent_hidden [R, d], frontier, pos, ctx_len [R] and kv_k, kv_v [R, ctx, d]

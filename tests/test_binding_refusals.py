@@ -20,3 +20,13 @@ def test_gemm_int4w_refuses_weights_on_the_cpu(block):
     q, s, z = block["wq"]
     with pytest.raises(lib.MtpError):
         lib.gemm_int4w(torch.zeros(1, 256, dtype=torch.bfloat16), q, s, z, group=64)
+
+
+def test_maps_in_another_form_need_no_bf16_ones():
+    """include/mtp.h: with FP8 or 4-bit maps the weights' own are not read and may be null."""
+    w = synth.make_draft_inputs(synth.DRAFT_SMALL, 1)["weights"]
+    rest = {k: v for k, v in w.items() if k not in lib.FP8_LINEAR_MAPS}
+    views = lib.ChainWeights(rest, 1, lib.FP8_LINEAR_MAPS).struct
+    assert views.hnorm[0] == w["hnorm"][0].data_ptr() and not views.wq and not views.w_down
+    with pytest.raises(KeyError):
+        lib.ChainWeights(rest, 1)
