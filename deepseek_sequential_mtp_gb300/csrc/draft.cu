@@ -868,6 +868,12 @@ DraftLayout draft_layout(const mtp_dims& D, int gamma, int prefix_len) {
   return L;
 }
 
+// sizes that the attention over the prefix takes; a position counts prefix and cache
+bool prefix_ok(const mtp_dims& D, int prefix_len) {
+  return prefix_len == 0 ||
+         (prefix_len > 0 && mtp::prefix_attn_sizes_ok(D.B, 1, D.n_heads, D.n_heads, D.head_dim, prefix_len, D.T));
+}
+
 bool draft_dims_ok(const mtp_dims& D) {
   return D.B > 0 && D.B <= kMaxR && D.T > 0 && D.d > 0 && D.d % 64 == 0 && D.n_heads > 0 &&
          (D.head_dim == 64 || D.head_dim == 128) && D.n_heads * D.head_dim == D.d && D.ffn > 0 && D.ffn % 8 == 0 &&
@@ -1081,7 +1087,7 @@ extern "C" size_t mtp_draft_round_workspace_bytes(const mtp_dims* dims, int gamm
 }
 
 extern "C" size_t mtp_draft_round_ext_workspace_bytes(const mtp_dims* dims, int gamma, int prefix_len) {
-  if (!dims || !draft_dims_ok(*dims) || gamma < 1 || gamma > kMaxRoundGamma || prefix_len < 0) return 0;
+  if (!dims || !draft_dims_ok(*dims) || gamma < 1 || gamma > kMaxRoundGamma || !prefix_ok(*dims, prefix_len)) return 0;
   return draft_layout(*dims, gamma, prefix_len).total;
 }
 
@@ -1110,6 +1116,7 @@ mtp_status draft_round_impl(const mtp_dims* dims, const mtp_weights* w, const mt
   if (ext.prefix_len < 0) return MTP_ERR_INVALID_ARG;
   if (ext.prefix_len > 0) {
     if (!ext.prefix_k || !ext.prefix_v) return MTP_ERR_INVALID_ARG;
+    if (!prefix_ok(D, ext.prefix_len)) return MTP_ERR_SHAPE;
     if (!mtp::aligned16(ext.prefix_k) || !mtp::aligned16(ext.prefix_v)) return MTP_ERR_ALIGNMENT;
   }
   if (i4) {

@@ -1260,21 +1260,21 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   return MTP_OK;
 }
 
-bool sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T) {
+}  // namespace
+
+bool prefix_attn_sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T) {
   return R >= 1 && R <= 65535 && L >= 1 && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H / Hkv <= kRows && (hd == 64 || hd == 128) && P >= 0 && T >= 0 &&
          static_cast<long long>(R) * L * H <= (1 << 24) && static_cast<long long>(P) + T <= 0x7FFFFF00ll;
 }
 
-}  // namespace
-
 size_t prefix_attn_workspace_bytes(int R, int L, int H, int Hkv, int hd, int P, int T) {
-  if (!sizes_ok(R, L, H, Hkv, hd, P, T)) return 0;
+  if (!prefix_attn_sizes_ok(R, L, H, Hkv, hd, P, T)) return 0;
   const long long rows = record_rows(make_shape(R, L, H, Hkv, P, T));
   return up256(rows * sizeof(float2)) + up256(static_cast<size_t>(rows) * hd * 4) + 256;
 }
 
 mtp_status prefix_attn_launch(const PrefixAttn& p, void* ws, size_t ws_bytes, cudaStream_t st) {
-  if (!sizes_ok(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_SHAPE;
+  if (!prefix_attn_sizes_ok(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_SHAPE;
   if (ws_bytes < prefix_attn_workspace_bytes(p.R, p.L, p.H, p.Hkv, p.hd, p.P, p.T)) return MTP_ERR_WORKSPACE;
   Shape s = make_shape(p.R, p.L, p.H, p.Hkv, p.P, p.T);
   s.causal = p.causal;
@@ -1295,7 +1295,7 @@ extern "C" mtp_status mtp_prefix_attention(const mtp_prefix_dims* d, const void*
                                            void* ws, size_t ws_bytes, cudaStream_t st) {
   if (!d) return MTP_ERR_INVALID_ARG;
   if (d->head_dim != 64 && d->head_dim != 128) return MTP_ERR_UNSUPPORTED;
-  if (!mtp::sizes_ok(d->R, d->L, d->n_heads, d->n_kv_heads, d->head_dim, d->P, d->T)) return MTP_ERR_SHAPE;
+  if (!mtp::prefix_attn_sizes_ok(d->R, d->L, d->n_heads, d->n_kv_heads, d->head_dim, d->P, d->T)) return MTP_ERR_SHAPE;
   if (!(d->scale >= 0.f) || d->scale > 3.0e38f) return MTP_ERR_INVALID_ARG;
   if (!q || !out || !ws || (d->P > 0 && (!prefix_k || !prefix_v)) || (d->T > 0 && (!kv_k || !kv_v))) return MTP_ERR_INVALID_ARG;
   const long long hd = d->head_dim, row = hd * d->n_kv_heads, q_row = hd * d->n_heads;

@@ -26,6 +26,7 @@ struct PrefixAttn {
   long long rec_stride = 0;
 };
 
+bool prefix_attn_sizes_ok(int R, int L, int H, int Hkv, int hd, int P, int T);
 size_t prefix_attn_workspace_bytes(int R, int L, int H, int Hkv, int hd, int P, int T);
 mtp_status prefix_attn_launch(const PrefixAttn& p, void* ws, size_t ws_bytes, cudaStream_t stream);
 

@@ -418,7 +418,8 @@ mtp_status mtp_draft_round(const mtp_dims* dims, const mtp_weights* w, const voi
  * those of dense tensors where 0: q [R, L, n_heads, head_dim], prefix_k and
  * prefix_v [P, n_kv_heads, head_dim], kv_k and kv_v [R, T, n_kv_heads, head_dim]
  * (head_dim is dense; any order of the others will do).
- * R <= 65535, n_heads / n_kv_heads <= 128, R * L * n_heads <= 2^24. */
+ * R <= 65535, n_heads / n_kv_heads <= 128, R * L * n_heads <= 2^24,
+ * P + T <= 2^31 - 256. */
 typedef struct mtp_prefix_dims {
   int R, L, n_heads, n_kv_heads, head_dim, P, T, causal;
   float scale;
@@ -518,7 +519,8 @@ typedef struct mtp_block_int4 {
  *   the cache holds them, of rows that precede every request's own cache (a
  *   prompt that the batch shares).  They are kept and read once for the batch;
  *   the result is that of caches which begin with these rows, to 2^-15 of the
- *   prefix's softmax weights.  pos may reach T + prefix_len. */
+ *   prefix's softmax weights.  pos may reach T + prefix_len, which is at
+ *   most 2^31 - 256. */
 typedef struct mtp_draft_ext {
   const mtp_block_fp8* fp8;
   const mtp_block_int4* int4;
