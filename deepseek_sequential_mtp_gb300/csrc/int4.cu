@@ -46,6 +46,7 @@ namespace {
 
 constexpr int kPitchPad = 64;           // two token rows' units fall into different banks
 constexpr int kMaxTokens = 32;
+constexpr int kMaxSize = 1 << 30;       // rows and columns, so that rounded-up counts stay within 31 bits
 
 // Variants by the number of 8-token tiles NT: with more than one, one CTA of 16
 // warps per SM shares the staged activations (16 tokens, 18432 x 7168: 28 us;
@@ -446,7 +447,8 @@ mtp_status plan(Args& a, const mtp::Int4Seg* segs, int group, cudaStream_t st) {
   a.wm = wm;
   a.cta_chunks = (a.chunks + C - 1) / C;
   // a piece is as many rounds of the k-warps as fit, at most the CTA's share
-  a.piece_chunks = (a.cta_chunks + wk - 1) / wk * wk;
+  // (no more than one token's activations alone would fill, so that the bytes stay within 31 bits)
+  a.piece_chunks = std::min((a.cta_chunks + wk - 1) / wk * wk, F::kSmem / F::kUnitBytes / wk * wk);
   while (a.piece_chunks > wk && piece_bytes<NT>(a.R, bm, a.piece_chunks, group) > F::kSmem) a.piece_chunks -= wk;
   const int smem = std::max(piece_bytes<NT>(a.R, bm, a.piece_chunks, group), wk * a.R * bm * 4);
   if (smem > F::kSmem) return MTP_ERR_UNSUPPORTED;  // not reached: one round fits for every R
@@ -482,6 +484,8 @@ mtp_status int4w_gemm_launch(const Int4Seg* segs, int nseg, int K, int group, co
   a.x = x;
   for (int i = 0; i < nseg; ++i)
     if (segs[i].n < 1) return MTP_ERR_SHAPE;
+  for (int i = 0; i < nseg; ++i)
+    if (segs[i].n > kMaxSize || K > kMaxSize) return MTP_ERR_UNSUPPORTED;
   return R <= 8 ? plan<1>(a, segs, group, st) : R <= 16 ? plan<2>(a, segs, group, st)
          : R <= 24 ? plan<3>(a, segs, group, st) : plan<4>(a, segs, group, st);
 }

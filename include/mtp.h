@@ -556,7 +556,7 @@ mtp_status mtp_gemm_fp8w(int R, int N, int K, const void* x, const void* wq, con
 /* Product of 1..32 tokens with a 4-bit weight matrix (the kernel the draft
  * step uses with 4-bit weights): out[R, N] (fp32, row stride N) = x[R, K] · W^T,
  * added to what out holds if `accumulate`.  x bf16; group 32, 64 or 128;
- * K % 32 == 0; x and w->q 16-byte aligned.  Products are exact in fp32, sums
+ * K % 32 == 0; N, K <= 2^30; x and w->q 16-byte aligned.  Products are exact in fp32, sums
  * and scales fp32, in an order fixed by the sizes: the result is the same every
  * time.  No workspace. */
 mtp_status mtp_gemm_int4w(int R, int N, int K, int group, const void* x, const mtp_int4_matrix* w, float* out,
