@@ -11,10 +11,8 @@
 // to fewer than 32 bits.  (On tcgen05, with the
 // unpacked weights in shared memory as the N = 256 side, 32 tokens take 49 us
 // instead of 42: each block is written and read there at four times its bytes.
-// e4m3 operands, for which a code is its
-// own byte, unpack in 3 instructions a word instead of 11, but mma.sync
-// executes them on this machine as two bf16-rate products after 17 more
-// instructions: 93 us instead of 43 on 7168 x 18432 with 32 tokens.)
+// With e4m3 operands, for which a code is its own byte, mma.sync takes 93 us
+// instead of 43 on 7168 x 18432 with 32 tokens.)
 //
 // The sum over k may be taken in any order, so a lane feeds the fragments
 // straight from its own 16 bytes: the quad that shares a weight row reads 64

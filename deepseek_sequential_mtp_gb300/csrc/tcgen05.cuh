@@ -116,9 +116,8 @@ __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 // The same products and the commit, called by a converged warp with the same arguments in
-// every lane; one lane, always the same, issues them.  Descriptors then stay in uniform
-// registers: 64 cycles per 128 x 128 x 16 product (the tensor core's rate), where one
-// thread's branch, which moves them there for each, takes 110 to 130.
+// every lane; one lane, always the same, issues them.  64 cycles per 128 x 128 x 16 product
+// (the tensor core's rate), where one thread's branch takes 110 to 130.
 __device__ __forceinline__ void umma_bf16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                   uint32_t accumulate) {
   asm volatile(
