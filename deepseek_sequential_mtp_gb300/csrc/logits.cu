@@ -9,8 +9,8 @@
 //   z(v) -= freq n(v) + pres [n(v) > 0];  z(v) += bias(v);  z(v) = -inf where the mask bit is 0
 //   p = softmax(z / temperature), or the one-hot of the lowest index of the maximum at temperature 0.
 //
-// Bound: HBM.  A row is read once (4 or 2 bytes a value and one mask bit) and
-// written once (4 bytes).  A cluster of C CTAs takes a row, each CTA a slice:
+// Bound: HBM.  A row has to be read once (4 or 2 bytes a value and one mask bit)
+// and written once (4 bytes).  A cluster of C CTAs takes a row, each CTA a slice:
 // pass 1 streams the slice and keeps a running maximum and sum per thread,
 // the cluster exchanges (maximum, sum), and pass 2 streams the slice again,
 // out of L2 (or out of registers, where one batch of loads covers it), and

@@ -15,9 +15,10 @@
  *     allocates nothing and keeps no state besides one device error word per
  *     translation unit (read with mtp_check_errors) and the tensor-map
  *     encoder entry point resolved on first use.
- *   - Calls are asynchronous on `stream`.  Inside one call, a GEMM may be
- *     launched as a programmatic dependent of the call's previous kernel (its
- *     setup overlaps that kernel; it reads nothing before it completes); the
+ *   - Calls are asynchronous on `stream`.  Inside one call, a GEMM or a kernel of
+ *     an attention may be launched as a programmatic dependent of the call's
+ *     previous kernel (its setup overlaps that kernel, or it runs beside it; it
+ *     reads nothing that the kernel writes before it completes); the
  *     first kernel of every call is an ordinary launch, so a call is ordered
  *     after all earlier work on `stream`.  Argument errors are detected on the
  *     host, return a status and launch nothing.  Data-dependent errors (token
@@ -309,7 +310,8 @@ typedef struct mtp_logits_params {
  *   status [R, L] int32 nullable = MTP_LOGITS_*; a row that is not OK is zero,
  *   which spec_verify reports as MTP_VERIFY_ZERO_RESIDUAL where it draws from
  *   it.  prm nullable (a plain softmax).  V <= 524288, L <= 65536.
- * Each row is read and written once; no workspace. */
+ * p is fp32: values below 2^-126 are 0.  A row is written once and read twice where
+ * it is longer than its CTAs hold (4096 values each); no workspace. */
 mtp_status mtp_logits_probs(int R, int L, int V, int dtype, const void* logits, long long ld,
                             const mtp_logits_params* prm, float* p, int32_t* status, cudaStream_t stream);
 
