@@ -66,6 +66,9 @@ def parse_args():
     ap.add_argument("--draft-gamma", type=int, default=4, help="steps of the recurrent draft round (<= 1: off)")
     ap.add_argument("--no-draft-fp8", dest="draft_fp8", action="store_false",
                     help="skip the draft step with FP8 block-scaled module weights")
+    ap.add_argument("--draft-int4", action="store_true", help="also the draft step with 4-bit module weights")
+    ap.add_argument("--draft-prefix", type=int, default=0,
+                    help="also the draft step on a prefix of that many rows that the requests share (0 = off)")
     ap.add_argument("--only-c3", action="store_true",
                     help="run only the DeepSeek-V3-width section (profiling its kernels) and print its record")
     ap.add_argument("--draft-requests", type=int, default=32,
@@ -792,6 +795,48 @@ def measure_draft(args, dev, rank, peaks):
                       "note": "module linear maps as e4m3 + fp32 128x128 block scales (1 B per weight); "
                               "head, norms and cache bf16"}
         del step8, out8, f8
+
+    # the step with 4-bit maps, and on a prefix that the requests share (with up to 256 rows of
+    # their own), with bf16 and with 4-bit maps
+    forms = {"int4": (0, True)} if args.draft_int4 else {}
+    if args.draft_prefix > 0:
+        forms["prefix"] = (args.draft_prefix, False)
+        if args.draft_int4:
+            forms["prefix_int4"] = (args.draft_prefix, True)
+    i4 = synth.make_int4_block(inp["weights"], 128) if args.draft_int4 else None
+    for name, (P, four) in forms.items():
+        fcfg = dataclasses.replace(cfg, ctx=min(cfg.ctx, 256)) if P else cfg
+        fstep = lib.DraftStep(fcfg, inp["weights"], device=dev, int4=i4 if four else None, prefix_len=P)
+        fin = {k: inp[k] for k in ("parent_hidden", "frontier", "pos", "kv_k", "kv_v", "ctx_len")}
+        if P:
+            fin.update({k: inp[k][:, :fcfg.ctx].contiguous() for k in ("kv_k", "kv_v")})
+            fin["ctx_len"] = (torch.arange(cfg.R, device=dev, dtype=torch.int32) * 37) % (fcfg.ctx + 1)
+            fin["pos"] = fin["ctx_len"] + P
+            gen = torch.Generator(device=dev).manual_seed(17 + rank)
+            fin.update({k: torch.randn((P, d), generator=gen, device=dev).to(torch.bfloat16)
+                        for k in ("prefix_k", "prefix_v")})
+        fout = {"q": torch.empty((cfg.R, cfg.V), dtype=torch.float32, device=dev),
+                "y": torch.empty(cfg.R, dtype=torch.int32, device=dev)}
+        for i in range(3):
+            fstep(**fin, seed=3, offset=i, out=fout)
+        torch.cuda.synchronize()
+        lib.check_errors()
+        ef = [(torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)) for _ in range(n)]
+        for i in range(n):
+            flush()
+            ef[i][0].record()
+            fstep(**fin, seed=3, offset=400 + i, out=fout)
+            ef[i][1].record()
+        torch.cuda.synchronize()
+        lib.check_errors()
+        t_ms = sorted(a.elapsed_time(b) for a, b in ef)[n // 2]
+        n_w = 2 * d * d + 4 * d * d + 3 * d * f
+        rows = P + int(fin["ctx_len"].sum()) if P else R * cfg.ctx
+        b_all = n_w * (0.5 + 2.0 / 128 if four else 2.0) + head_bytes + 2.0 * 2 * rows * d + q_bytes
+        res[name] = {"ms_median": t_ms, "algorithmic_bytes": b_all, "achieved_gbs": b_all / (t_ms / 1e3) / 1e9,
+                     "frac": b_all / (t_ms / 1e3) / 1e9 / hbm_peak, "steps": n}
+        del fstep, fin, fout
+    del i4
 
     # recurrent round of gamma draft steps, then gamma-position verification of its draws
     g = args.draft_gamma

@@ -7,13 +7,14 @@
 // and the parts joined at the end: o = Σ 2^(m_p - M) o_p / Σ 2^(m_p - M) l_p.
 //
 // Bound: HBM for few rows (the keys and values once: 4 hd bytes per key and
-// head), the tensor cores once some 300 rows share a head's prefix.  Measured, call
+// head), the tensor cores once some 200 rows share a head's prefix (the weights' two
+// parts make it three products instead of two).  Measured, call
 // after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
 // to 256 own keys 76 us (4.6 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
-// 63 us (4.2 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
+// 62 us (4.3 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
 // to 512 own keys 66 us (336 TFLOP/s).  Each further key of such a prefix costs its
-// bytes at 6.6 TB/s in the first case, at 5.4 in the second, and 900 TFLOP/s in the
-// third; the rest is three kernels' way to their first data, one after the other.
+// bytes at 6.9 TB/s in the first two cases, and 760 TFLOP/s (of the two products of the
+// formula) in the third; the rest is three kernels' way to their first data, one after the other.
 //
 // All rows that see the same keys form one matrix: for the prefix the R L G rows
 // (G = query heads per key head) of all requests, for a request's own cache its
@@ -42,18 +43,20 @@
 // A last block is loaded as 64 rows where it has no more, and its products run over
 // as many groups of 16 keys as it has.
 //
-// Few rows (small_attn_kernel): own caches with up to 32 rows per key head, and a
-// prefix with up to 16 in all.  The kernel above spends 3.5 us on an item of one or
-// two blocks, whatever its rows: the chain load, S, softmax, P V has two tiles to
-// overlap with, and most of each is padding.  Here a warp takes 16 rows and 16 keys
-// with mma.sync.m16n8k16, and as many chains run as there are warps.  Calls with own
-// caches alone, against the kernel above: 32 requests, 56 heads, 256 keys 59 us
-// instead of 83, 32 heads over 8 with 5 tokens (20 rows), 512 keys 32 instead of 42,
-// 64 over 8 with 4 (32 rows) 37 instead of 43, 2048 keys 76 instead of 78; a prefix
-// of 8192 keys and 16 rows 63 instead of 65, of 300 keys and 4 rows 13.4 instead of
-// 15.5.  A prefix with 32 rows gains nothing (52 us both), own caches with more rows
-// have tiles to fill.  It is launched beside the kernel above, whose CTAs fill an SM,
-// and takes the SMs as they become free.
+// Few rows (small_attn_kernel): own caches with up to 32 rows per key head (8 beside a
+// prefix on row tiles), and a prefix with up to 16 in all.  The kernel above spends
+// 3.5 us on an item of one or two blocks, whatever its rows: the chain load, S, softmax,
+// P V has two tiles to overlap with, and most of each is padding.  Here a warp takes 16
+// rows and 16 keys with mma.sync.m16n8k16, and as many chains run as there are warps.
+// Replayed from a graph, against the kernel above: own caches alone, 32 requests, 56
+// heads, 256 keys 45 us instead of 69, 32 heads over 8 with 5 tokens (20 rows), 512 keys
+// 26 instead of 32, 64 over 8 with 4 (32 rows) 31 instead of 34, 2048 keys 67 instead of
+// 63.  Beside a prefix of 8192 keys on row tiles it is a launch more: up to 1024 keys, 56
+// heads of one row 117 us instead of 145, 8 heads of 4 rows 38 and 39, 8 rows 45 and 43,
+// 16 59 and 55, 20 71 and 65.  A prefix of 8192 keys, 56 heads and 16 rows 46 instead of
+// 49, one row 42 instead of 47, 16 heads, 300 keys and 4 rows 5 instead of 9, but 8 heads
+// of 16 rows on 65000 keys 55 instead of 52; with 32 rows 53 instead of 50.  It is launched
+// beside the kernel above, whose CTAs fill an SM, and takes the SMs as they become free.
 //
 // Keys past a request's ctx_len may hold anything: their scores are replaced, and
 // their V rows are cleared in shared memory (0 times NaN is NaN); rows of new tokens that
@@ -84,9 +87,9 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 // costs for the deal: a block with one row tile, with two, and what a segment
 // of a request's own cache costs besides
 constexpr int kCostOne = 6, kCostTwo = 11, kCostItem = 5;
-// the small-row kernel: rows that it takes of a prefix, of an own cache; log2 of its
-// blocks' keys, keys of a box
-constexpr int kSmallPrefix = 16, kSmallOwn = 32, kSmallShift = 6, kSmallBox = 32, kSmallCost = 2, kSmallCostItem = 1;
+// the small-row kernel: rows that it takes of a prefix, of an own cache alone and beside a
+// prefix on row tiles; log2 of its blocks' keys, keys of a box
+constexpr int kSmallPrefix = 16, kSmallOwn = 32, kSmallOwnBeside = 8, kSmallShift = 6, kSmallBox = 32, kSmallCost = 2, kSmallCostItem = 1;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -943,9 +946,8 @@ small_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scale
 // ctx_len alone, so all of that runs under the kernels before; what is left then is one
 // chain of loads, in which the first records' outputs are asked for with their maxima.
 constexpr int kJoinWarps = 4;
-// Up to this many rows per SM have a CTA each: with 128 rows of 150 records a call takes 72 us
-// instead of 85, with 512 of 60 36 instead of 40; with 1792 of 12 111 instead of 108, with 5120 of
-// 20 85 instead of 75.
+// Up to this many rows per SM have a CTA each: 128 rows (65000 keys) 56 us a call instead of 68,
+// 512 60 instead of 61; 1792 (8192 keys) 93 instead of 90, 5120 83 instead of 72.
 constexpr int kSplitRows = 8;
 // what the join needs of the own caches where it takes them up itself (see_again)
 struct OwnRows {
@@ -1171,8 +1173,9 @@ Shape make_shape(int R, int L, int H, int Hkv, int P, int T) {
   s.own_items = (s.groups + 1) / 2;
   s.own_rec = s.tokens * s.G;
   s.prefix_rec = s.requests * s.own_rec;
-  s.own_small = T > 0 && static_cast<long long>(L) * s.G <= kSmallOwn ? (L * s.G + 15) / 16 : 0;
   s.prefix_small = P > 0 && static_cast<long long>(R) * L * s.G <= kSmallPrefix;
+  const int most = P > 0 && !s.prefix_small ? kSmallOwnBeside : kSmallOwn;
+  s.own_small = T > 0 && static_cast<long long>(L) * s.G <= most ? (L * s.G + 15) / 16 : 0;
   s.prefix_per = s.prefix_small ? 4 : 2;
   s.own_per = s.own_small ? 4 : 2;
   s.prefix_blocks = blocks_of(P, s.prefix_small ? kSmallShift : 7);
