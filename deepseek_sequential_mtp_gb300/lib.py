@@ -703,11 +703,12 @@ class _Draft:
         self.weights = {k: v for k, v in weights.items() if k not in without}
         d, f = cfg.d, cfg.ffn
         shapes = {"embed": (cfg.V, d), "head": (cfg.V, d), "out_norm": (d,), "hnorm": (d,), "enorm": (d,),
-                  "attn_norm": (d,), "ffn_norm": (d,), "eh_proj": (d, 2 * d), "w_gate": (f, d), "w_up": (f, d),
-                  "w_down": (d, f)}
-        for name, t in self.weights.items():
+                  "attn_norm": (d,), "ffn_norm": (d,), "eh_proj": (d, 2 * d), "wq": (d, d), "wk": (d, d),
+                  "wv": (d, d), "wo": (d, d), "w_gate": (f, d), "w_up": (f, d), "w_down": (d, f)}
+        for name, shape in shapes.items():
+            t = self.weights.get(name, ())
             for m in t if isinstance(t, (list, tuple)) else (t,):
-                _arg(m, f"weights[{name!r}]", torch.bfloat16, shapes.get(name, (d, d)), self.weights["embed"].device)
+                _arg(m, f"weights[{name!r}]", torch.bfloat16, shape, self.weights["embed"].device)
         self.w = ChainWeights(self.weights, 1, without)
         self.f8 = Fp8Block(fp8) if fp8 is not None else None
         self.i4 = Int4Block(int4, int4_group, cfg) if int4 is not None else None

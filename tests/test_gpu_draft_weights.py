@@ -41,4 +41,5 @@ def test_weights_are_checked():
             lib.DraftStep(CFG, {**w, name: bad})
     with pytest.raises(lib.MtpError):
         lib.DraftStep(CFG, w, device="cpu")
+    lib.DraftStep(CFG, {**w, "another": torch.zeros(3)})  # not the step's
     lib.DraftStep(CFG, {**w, "wq": [w["wq"][0].cpu()]}, int4=i4, int4_group=64)  # not read
