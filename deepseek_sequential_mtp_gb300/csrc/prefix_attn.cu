@@ -10,7 +10,7 @@
 // head), the tensor cores once some 200 rows share a head's prefix (the weights' two
 // parts make it three products instead of two).  Measured, call
 // after call on inputs out of HBM: 32 requests, 56 heads of 128, 8192 shared and up
-// to 256 own keys 76 us (4.6 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
+// to 256 own keys 77 us (4.5 TB/s); 6 requests, 64 heads over 8, 65000 shared keys
 // 62 us (4.3 TB/s); 5 new tokens of 32 requests, 32 heads over 8, 8192 shared and up
 // to 512 own keys 66 us (336 TFLOP/s).  Each further key of such a prefix costs its
 // bytes at 6.9 TB/s in the first two cases, and 760 TFLOP/s (of the two products of the
@@ -949,6 +949,13 @@ constexpr int kJoinWarps = 4;
 // Up to this many rows per SM have a CTA each: 128 rows (65000 keys) 56 us a call instead of 68,
 // 512 60 instead of 61; 1792 (8192 keys) 93 instead of 90, 5120 83 instead of 72.
 constexpr int kSplitRows = 8;
+template <int kD>
+__device__ __forceinline__ void store_row(__nv_bfloat16* to, const float (&acc)[kD], float inv) {
+  if constexpr (kD == 4)
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(to) = pack2_bf16(acc[0] * inv, acc[1] * inv);
+}
 // what the join needs of the own caches where it takes them up itself (see_again)
 struct OwnRows {
   const __nv_bfloat16 *q, *k, *v;
@@ -969,11 +976,15 @@ __device__ __forceinline__ void load_bf16(const __nv_bfloat16* p, float (&f)[kD]
 // `see` rows of its own cache, one at a time, by a warp.  The products take 16 keys of all the
 // rows together, with a weight of 0 where a row does not see a key, and 0 times the NaN or the
 // infinity that a later token's value may hold (a padded draft's) is NaN.  The maxima and
-// sums are free of it; where an output is not finite, it is worked out again from what it sees.
+// sums are free of it; where an output is not finite, it is worked out again from what it sees
+// (5 tokens of 32 requests, 512 own keys, half of the requests padded: 191 us instead of 70).
+// (A function of its own that writes the row, in a form of the join for such calls: within
+// it, or in every form, it cost the others 1 to 1.5 us.)
 template <int kD>
-__device__ __forceinline__ void see_again(float (&acc)[kD], const OwnRows& own, const float2* rec_ml, const float* rec_o,
-                                       long long at0, int step0, int n0, int r, int i, int h, int head, int see, float M,
-                                       int lane) {
+__device__ __noinline__ void see_again(const OwnRows& own, const float2* rec_ml, const float* rec_o, long long at0, int step0,
+                                       int n0, int r, int i, int h, int head, int see, float M, float L, __nv_bfloat16* to) {
+  const int lane = threadIdx.x & 31;
+  float acc[kD];
 #pragma unroll
   for (int d = 0; d < kD; ++d) acc[d] = 0.f;
 #pragma unroll 1
@@ -988,20 +999,33 @@ __device__ __forceinline__ void see_again(float (&acc)[kD], const OwnRows& own, 
   float q[kD];
   load_bf16<kD>(own.q + r * own.q_r + i * own.q_l + h * own.q_h + lane * kD, q);
   const long long at = r * own.k_r + head * own.k_h + lane * kD;
+  constexpr int kU = 4;  // keys whose loads and sums are under way together
 #pragma unroll 1
-  for (int j = 0; j < see; ++j) {
-    float k[kD], v[kD], s = 0.f;
-    load_bf16<kD>(own.k + at + j * own.k_t, k);
-    load_bf16<kD>(own.v + at + j * own.k_t, v);
+  for (int j0 = 0; j0 < see; j0 += kU) {
+    float v[kU][kD], s[kU];
 #pragma unroll
-    for (int d = 0; d < kD; ++d) s = fmaf(q[d], k[d], s);
-    const float w = ex2(fmaf(warp_sum(s), own.scale_log2, -M));
+    for (int u = 0; u < kU; ++u) {
+      float k[kD];
+      const long long row = at + min(j0 + u, see - 1) * own.k_t;
+      load_bf16<kD>(own.k + row, k);
+      load_bf16<kD>(own.v + row, v[u]);
+      s[u] = 0.f;
 #pragma unroll
-    for (int d = 0; d < kD; ++d) acc[d] = fmaf(w, v[d], acc[d]);
+      for (int d = 0; d < kD; ++d) s[u] = fmaf(q[d], k[d], s[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float w = ex2(fmaf(warp_sum(s[u]), own.scale_log2, -M));
+      if (j0 + u < see) {
+#pragma unroll
+        for (int d = 0; d < kD; ++d) acc[d] = fmaf(w, v[u][d], acc[d]);
+      }
+    }
   }
+  store_row<kD>(to, acc, 1.f / L);
 }
 
-template <int HD, int kSplit>
+template <int HD, int kSplit, bool kLater>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 prefix_join_kernel(const Shape sh, const __grid_constant__ OwnRows own, const float2* __restrict__ rec_ml,
                    const float* __restrict__ rec_o, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, float* __restrict__ rec, long long rec_stride) {
@@ -1127,13 +1151,6 @@ prefix_join_kernel(const Shape sh, const __grid_constant__ OwnRows own, const fl
       for (int d = 0; d < kD; ++d) acc[d] += f * s_o[w][lane * kD + d];
     }
   }
-  if (sh.causal && nb > 0 && i + 1 < sh.L) {  // rows of later tokens stand beside this one's
-    bool odd = false;
-#pragma unroll
-    for (int d = 0; d < kD; ++d) odd |= !(fabsf(acc[d]) < INFINITY);
-    if (__any_sync(0xffffffffu, odd) && L == L)
-      see_again<kD>(acc, own, rec_ml, rec_o, at0, step0, n0, r, i, h, head, max(0, sh.ctx(r) - sh.L + 1 + i), M, lane);
-  }
   const long long out = (static_cast<long long>(r) * sh.L + i) * sh.H + h;
   if (rec) {
     float* to = rec + out * rec_stride;
@@ -1147,11 +1164,17 @@ prefix_join_kernel(const Shape sh, const __grid_constant__ OwnRows own, const fl
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;  // a row that sees no key: zeros
   __nv_bfloat16* to = o + out * HD + lane * kD;
-  if constexpr (kD == 4)
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(to) = pack2_bf16(acc[0] * inv, acc[1] * inv);
+  store_row<kD>(to, acc, inv);
   if (lse && lane == 0) lse[out] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+  if constexpr (kLater) {
+    if (nb > 0 && i + 1 < sh.L) {  // rows of later tokens stood beside this one's
+      bool odd = false;
+#pragma unroll
+      for (int d = 0; d < kD; ++d) odd |= !(fabsf(acc[d]) < INFINITY);
+      if (__any_sync(0xffffffffu, odd) && L == L)
+        see_again<kD>(own, rec_ml, rec_o, at0, step0, n0, r, i, h, head, max(0, sh.ctx(r) - sh.L + 1 + i), M, L, to);
+    }
+  }
 }
 
 inline size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
@@ -1252,7 +1275,9 @@ mtp_status launch(const PrefixAttn& p, const Shape& s, float2* ml, float* ro, cu
   // few rows: their records by four warps each
   const bool split = static_cast<long long>(s.R) * s.L * s.H <= kSplitRows * sm_count_current();
   const dim3 grid(split ? s.L * s.H : (s.L * s.H + kJoinWarps - 1) / kJoinWarps, s.R);
-  auto join = split ? prefix_join_kernel<HD, kJoinWarps> : prefix_join_kernel<HD, 1>;
+  const bool later = s.causal && s.L > 1 && p.T > 0;
+  auto join = split ? (later ? prefix_join_kernel<HD, kJoinWarps, true> : prefix_join_kernel<HD, kJoinWarps, false>)
+                    : (later ? prefix_join_kernel<HD, 1, true> : prefix_join_kernel<HD, 1, false>);
   const OwnRows own{p.q, p.kk, p.kv, p.q_r, p.q_l, p.q_h, p.k_r, p.k_t, p.k_h, scale_log2};
   if (p.P > 0 || p.T > 0)
     MTP_CUDA_TRY(launch_pdl(join, grid, dim3(32 * kJoinWarps), 0, st, s, own, ml, ro, p.o, p.lse, p.rec, p.rec_stride));
