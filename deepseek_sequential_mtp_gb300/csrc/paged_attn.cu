@@ -820,7 +820,7 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
   } else {
     // Softmax.  After an abort everything runs on (the waits return at once), so that the groups'
     // barriers meet.
-    constexpr int kPitch = 528;  // of two rows' 128 scores
+    constexpr int kPitch = 68;  // of a row's 64 numbers
     const int x = warp >> 2, j = threadIdx.x & 127, w4 = warp & 3;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t s_at = lanes + x * C::kSCols, o_at = lanes + C::kColO + x * C::kOCols, l_at = lanes + C::kColL + x * kMax;
@@ -837,8 +837,6 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
     uint32_t* unset = need + 3;
     uint8_t* p_group = smem + C::kOffP + x * C::kPBytes;
     uint8_t* p_to = p_group + (j >> 3) * 128 + (j & 7) * 16;
-    // threads that look over two rows: a power of two that leaves enough of them, 128 numbers at most
-    const int per_pair = NR <= 8 ? 32 : NR <= 16 ? 16 : NR <= 32 ? 8 : 4;
     if (j < 3) need[j] = 0;
     if (j < kMax) largest[j] = 0;
     uint32_t g = 0, third = 0;
@@ -919,29 +917,30 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
         if (which) {
           // Rows of these chunks whose scores are over the top, or that have no reference yet, get one.
           if (forced) {
-            // maxima of two rows at a time, as bf16, by way of the weights' buffer.  (No shuffles: in a branch that may part the
-            // warp, as far as the compiler knows, each takes 230 cycles.)
+            // maxima of two lanes together, then of 64 numbers a row by way of the weights' buffer
+            float* put = reinterpret_cast<float*>(p_group);
 #pragma unroll 1
             for (int c = 0; c < NR; c += 8) {
               if (!(forced >> (c / 8) & 1)) continue;
               float z[8];
               exponents(c, z);
 #pragma unroll
-              for (int i = 0; i < 8; i += 2)
-                *reinterpret_cast<uint32_t*>(p_group + (c + i) / 2 * kPitch + 4 * j) = pack2_bf16(z[i] + d, z[i + 1] + d);
+              for (int i = 0; i < 8; ++i) {
+                const float s = fmaxf(z[i] + d, __shfl_xor_sync(0xffffffffu, z[i] + d, 16));
+                if (lane < 16) put[(c + i) * kPitch + w4 * 16 + lane] = s;
+              }
             }
             group_sync(x);
-            const int pair = j / per_pair, part = j % per_pair;
-            if (2 * pair < NR && (forced >> (pair / 4) & 1)) {
-              __nv_bfloat162 top = __float2bfloat162_rn(-INFINITY);
-#pragma unroll 1
-              for (int i = part; i < 32; i += per_pair) {
-                const uint4 v = *reinterpret_cast<const uint4*>(p_group + pair * kPitch + i * 16);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int i = j; i < NR * 4; i += 128) {
+              if (!(forced >> (i / 32) & 1)) continue;
+              const float4* from = reinterpret_cast<const float4*>(put + i / 4 * kPitch) + i % 4;
+              float top = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = __hmax2(top, *reinterpret_cast<const __nv_bfloat162*>(&w[e]));
+              for (int e = 0; e < 4; ++e) {
+                const float4 v = from[4 * e];
+                top = fmaxf(top, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
               }
-              *reinterpret_cast<float2*>(parts + part * NR + 2 * pair) = __bfloat1622float2(top);
+              parts[i % 4 * NR + i / 4] = top;
             }
             group_sync(x);
           }
@@ -952,15 +951,15 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
               bare = unset[w4] >> lane & 1;
               float top = -INFINITY;
               if (bare) {
-                for (int i = 0; i < per_pair; ++i) top = fmaxf(top, parts[i * NR + j]);
-                top += fabsf(top) * 0x1p-7f;  // (the rounding to bf16)
+                top = fmaxf(fmaxf(parts[j], parts[NR + j]), fmaxf(parts[2 * NR + j], parts[3 * NR + j]));
               } else if (largest[j] != 0) {
                 top = __int_as_float(largest[j]);
               }
               largest[j] = 0;
               if (top > -INFINITY) {
-                rows[j].y += kTopLog2 - top;
-                by = bare ? 0.f : kTopLog2 - top;  // (a row without a reference has nothing to shrink)
+                const float was = rows[j].y, now = was + (kTopLog2 - top);
+                rows[j].y = now;
+                by = bare ? 0.f : now - was;  // (a row without a reference has nothing to shrink; `now` is rounded)
                 bare = false;
               }
             }
@@ -1076,12 +1075,12 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float s = l[i] + __shfl_xor_sync(0xffffffffu, l[i], 16);
-            if (lane < 16) put[(c + i) * 68 + w4 * 16 + lane] = s;
+            if (lane < 16) put[(c + i) * kPitch + w4 * 16 + lane] = s;
           }
         }
         group_sync(x);
         for (int i = j; i < NR * 4; i += 128) {
-          const float4* from = reinterpret_cast<const float4*>(put + i / 4 * 68) + i % 4;
+          const float4* from = reinterpret_cast<const float4*>(put + i / 4 * kPitch) + i % 4;
           const float4 a = from[0], b = from[4], c = from[8], e = from[12];
           parts[i % 4 * NR + i / 4] = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + (((c.x + c.y) + (c.z + c.w)) + ((e.x + e.y) + (e.z + e.w)));
         }
