@@ -430,7 +430,7 @@ paged_rows_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, float 
 // cache's codes are the operands with M = 128, as TMA brings them, and the few rows are N.
 // kind::f8f6f4 takes codes on both sides: a query row is 2^up (hi + lo), two products
 // into one sum; a weight w <= 448 is a + 2^-4 b + 2^-9 c in columns and accumulators of their own (fp16's
-// precision, and 2^-23 of the largest weight at the least).  A thread has a key, whose
+// precision, and off by 2^-26 of the largest weight at the most).  A thread has a key, whose
 // block's scales are numbers of its own, and goes over the rows.
 //   two or three groups of four warps: softmax of every second or third block, each with a reference, a sum and an
 //                 output of its own (parts)
@@ -439,8 +439,12 @@ paged_rows_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, float 
 //   query warp    turns a segment's queries into codes, a segment ahead
 //   page warp     walks ahead and looks up the blocks' pages and exponents
 constexpr int kCols = 128;                 // keys of a block
-constexpr float kTopLog2 = 4.0f;           // a weight is 2^4 at the reference
-constexpr float kSlackLog2 = 4.8f;         // and at most 448
+// A weight is 2^7 at the reference and at most 448; the codes' least step is 2^-18.  Weights below half of it leave the outputs, not
+// the sums: n keys share less than n 2^-26 of the largest that way.  (2^4 and 4.8 bits of slack: references are raised more seldom, 117
+// us instead of 120 for 5 tokens of 64 requests and 438 instead of 441 for one of 32, but weights end at 2^-23: 11000 keys at 2^-23.7
+// of the largest had no share in the outputs.)
+constexpr float kTopLog2 = 7.0f;
+constexpr float kSlackLog2 = 1.8f;
 // kMax: rows that a tile may have; the launch's, a multiple of 8, are a number of its own (loops over them are
 // not unrolled: unrolled ones were bound by the fetching of instructions, 1130 us instead of 895 for 1024 tokens of two prompts).
 template <int HD, int kMax>
@@ -825,7 +829,7 @@ paged_cols_kernel(const __grid_constant__ PagedMaps maps, const Shape sh, int bo
     const uint32_t lanes = tmem + (static_cast<uint32_t>(w4 * 32) << 16);
     const uint32_t s_at = lanes + x * C::kSCols, o_at = lanes + C::kColO + x * C::kOCols, l_at = lanes + C::kColL + x * kMax;
     const uint32_t every = (1u << (NR / 8)) - 1;  // chunks of 8 rows
-    // of the group: a row's scale and what is added to its scores (4 - reference); what its weights shrink by; its largest exponent
+    // of the group: a row's scale and what is added to its scores (7 - reference); what its weights shrink by; its largest exponent
     // over the top (0: none); parts' maxima or sums; a second factor for references that values' scales put further apart than a
     // float's exponent holds; chunks over the top in three turns; rows without a reference, and whether any has a second factor
     float2* rows = reinterpret_cast<float2*>(smem + C::kOffMax + x * C::kGroupBytes);
