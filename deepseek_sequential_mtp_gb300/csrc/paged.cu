@@ -641,7 +641,7 @@ extern "C" mtp_status mtp_rope_frequencies(int rot, double base, int scaling, do
   if (scaling == MTP_ROPE_YARN) {  // index of the pair that turns so many times within `original` positions
     const auto at = [&](double turns) { return rot * std::log(original / (turns * two_pi)) / (2.0 * std::log(base)); };
     low = std::fmax(std::floor(at(beta_fast)), 0.0);
-    high = std::fmin(std::ceil(at(beta_slow)), n - 1.0);
+    high = std::fmin(std::ceil(at(beta_slow)), rot - 1.0);  // (behind the last pair too: the ramp's slope is the method's)
     high = std::fmax(high, low + 1e-3);
   }
   for (int p = 0; p < n; ++p) {

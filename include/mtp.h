@@ -481,7 +481,9 @@ typedef struct mtp_rotation {
  *   LINEAR  that / factor;
  *   YARN    pairs that turn less than beta_slow times within `original` positions
  *           / factor, those that turn more than beta_fast times as they are, linear in
- *           the pair's index between; mscale = 0.1 ln(factor) + 1;
+ *           the pair's index between; mscale = 0.1 ln(factor) + 1.  The index that turns so
+ *           many times, rot ln(original / (2 pi turns)) / (2 ln base), is rounded down for
+ *           beta_fast and up for beta_slow, and kept within 0 and rot - 1;
  *   BANDS   pairs whose wavelength is above original / low / factor, those below
  *           original / high as they are, linear in original / wavelength between
  *           (beta_slow = low, beta_fast = high). */
