@@ -756,9 +756,9 @@ class _Draft:
         self.i4 = Int4Block(int4, int4_group, cfg) if int4 is not None else None
         self.paged = None
         if paged is not None:
-            self.pages = paged
-            self.paged = _paged(*(paged.get(k) for k in ("k_pages", "v_pages", "page_table", "k_scale", "v_scale")),
-                                self.weights["embed"].device)
+            # (the tensors, not the caller's dict: their addresses are taken here, once)
+            self.pages = {k: paged.get(k) for k in ("k_pages", "v_pages", "page_table", "k_scale", "v_scale")}
+            self.paged = _paged(*self.pages.values(), self.weights["embed"].device)
             c = self.paged
             if (c.n_kv_heads, c.head_dim, c.table_len * c.page) != (cfg.n_heads, cfg.head_dim, cfg.ctx) or \
                     paged["page_table"].shape[0] != cfg.R:
@@ -846,7 +846,8 @@ class DraftStep(_Draft):
     share its workspace and must not overlap.
 
     ``paged``: the caches are pages, {"k_pages", "v_pages", "page_table"} and in 8 bits {"k_scale",
-    "v_scale"} as kv_append takes them, of n_heads heads and ctx tokens per request; kv_k and kv_v are None then, and
+    "v_scale"} as kv_append takes them, of n_heads heads and ctx tokens per request.  The object keeps these tensors: a page
+    table changes in place (copy_), another entry of the dict is not seen.  kv_k and kv_v are None then, and
     ``rows_out`` {"k", "v"} [R, steps, n_heads, head_dim] receives the steps' rotated keys and values, for
     kv_append (include/mtp.h: mtp_draft_round_paged)."""
 
