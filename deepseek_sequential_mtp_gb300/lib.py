@@ -847,7 +847,8 @@ class DraftStep(_Draft):
 
     ``paged``: the caches are pages, {"k_pages", "v_pages", "page_table"} and in 8 bits {"k_scale",
     "v_scale"} as kv_append takes them, of n_heads heads and ctx tokens per request.  The object keeps these tensors: a page
-    table changes in place (copy_), another entry of the dict is not seen.  kv_k and kv_v are None then, and
+    table changes in place (copy_), another entry of the dict is not seen.  Its keys must be turned as the step turns its own:
+    rope_frequencies(head_dim, rope_base) in halves, without scaling.  kv_k and kv_v are None then, and
     ``rows_out`` {"k", "v"} [R, steps, n_heads, head_dim] receives the steps' rotated keys and values, for
     kv_append (include/mtp.h: mtp_draft_round_paged)."""
 

@@ -696,6 +696,11 @@ size_t mtp_draft_round_paged_workspace_bytes(const mtp_dims* dims, int gamma, in
  * in the place of kv_k and kv_v: n_kv_heads = n_heads, head_dim the module's, and
  * dims->T = table_len * page.  Request r attends to its first ctx_len[r] rows there
  * (mtp_paged_attention's precision), the round's own rows and the prefix, if any.
+ * The step turns its own q and k as the chain does: whole heads in halves, frequencies
+ * rope_base^(-2p/head_dim), factor 1 (rope_base = 0: not at all).  The cache's keys must have been
+ * turned in that way (mtp_rope_frequencies NONE with rot = head_dim, not interleaved): with keys
+ * that were turned by scaled frequencies, as neighbours or in part the scores are wrong, and nothing
+ * reports it.
  *   rows_k, rows_v [R, gamma, d] bf16, nullable (both or none), 16-byte aligned: receive the
  *   round's rotated keys and values; those of the drafts that verification keeps go into the
  *   cache by mtp_kv_append without a rotation (n_new: how many). */
