@@ -584,6 +584,17 @@ mtp_status rotation_check(const mtp_rotation* rot, int head_dim) {
   if (reinterpret_cast<uintptr_t>(rot->inv_freq) & 7u) return MTP_ERR_ALIGNMENT;
   return MTP_OK;
 }
+// whether two rows of hd elements at n on + h oh, n < N and h < H, share one
+bool rows_meet(long long N, long long H, int hd, long long on, long long oh) {
+  if ((N > 1 && on < hd) || (H > 1 && oh < hd)) return true;
+  if (N == 1 || H == 1) return false;
+  if (on > oh ? on - hd >= (H - 1) * oh : oh - hd >= (N - 1) * on) return false;  // one within a step of the other
+  for (long long h = 1; h < H; ++h) {  // the two rows n below and above h oh
+    const long long n = h * oh / on, over = h * oh - n * on;
+    if ((n < N && over < hd) || (n + 1 < N && on - over < hd)) return true;
+  }
+  return false;
+}
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -673,8 +684,7 @@ extern "C" mtp_status mtp_rope(long long N, int H, int head_dim, int dtype, cons
   if (oh == 0) oh = head_dim;
   if (on == 0) on = dense;
   if (xn < 0 || xh < 0 || on < 0 || oh < 0) return MTP_ERR_SHAPE;
-  if ((N > 1 && H > 1 && (on < oh ? on < head_dim : oh < head_dim)) || (H > 1 && oh < head_dim) || (N > 1 && on < head_dim))
-    return MTP_ERR_SHAPE;  // rows of out on top of one another
+  if (rows_meet(N, H, head_dim, on, oh)) return MTP_ERR_SHAPE;
   const int bytes = dtype == MTP_F32 ? 4 : 2;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out)) & (bytes - 1)) return MTP_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(pos) & 3u) return MTP_ERR_ALIGNMENT;

@@ -495,7 +495,7 @@ mtp_status mtp_rope_frequencies(int rot, double base, int scaling, double factor
  * gradients of the turned rows into gradients of the rows (backward = 1: the angles
  * negated).  dtype MTP_F32 or MTP_BF16; head_dim even, up to 1024; strides count elements,
  * 0 are those of dense rows; out may be x itself (with the same strides) and must not
- * overlap it otherwise.  pos may be negative.  Arithmetic in fp32. */
+ * overlap it otherwise, nor may out's rows overlap one another.  pos may be negative.  Arithmetic in fp32. */
 mtp_status mtp_rope(long long N, int H, int head_dim, int dtype, const mtp_rotation* rotation, const int32_t* pos,
                     int backward, const void* x, long long x_stride_n, long long x_stride_h, void* out,
                     long long out_stride_n, long long out_stride_h, cudaStream_t stream);
