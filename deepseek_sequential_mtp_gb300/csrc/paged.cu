@@ -595,6 +595,11 @@ bool rows_meet(long long N, long long H, int hd, long long on, long long oh) {
   }
   return false;
 }
+// whether [a, a + a_bytes) and [b, b + b_bytes) share a byte
+bool ranges_meet(const void* a, unsigned long long a_bytes, const void* b, unsigned long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + b_bytes && y < x + a_bytes;
+}
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -762,6 +767,15 @@ extern "C" mtp_status mtp_kv_append(const mtp_paged_cache* cache, const mtp_kv_r
   if (w.q == w.q_out && w.q && (w.q_stride_h != hd || w.q_stride_t != static_cast<long long>(w.n_heads) * hd ||
                                 w.q_stride_r != static_cast<long long>(w.L) * w.n_heads * hd))
     return MTP_ERR_INVALID_ARG;
+  if (w.q) {  // q_out is written while other blocks read
+    const auto span = [&](long long heads, long long sr, long long st, long long sh) {
+      return 2ull * ((w.R - 1) * sr + (w.L - 1) * st + (heads - 1) * sh + hd);
+    };
+    const unsigned long long out = 2ull * w.R * w.L * w.n_heads * hd, kv = span(Hkv, w.kv_stride_r, w.kv_stride_t, w.kv_stride_h);
+    if (ranges_meet(w.q_out, out, w.k, kv) || ranges_meet(w.q_out, out, w.v, kv) ||
+        (w.q != w.q_out && ranges_meet(w.q_out, out, w.q, span(w.n_heads, w.q_stride_r, w.q_stride_t, w.q_stride_h))))
+      return MTP_ERR_INVALID_ARG;
+  }
   const bool turned = rotation && rotation->inv_freq;
   g.rot = turned ? rotation->rot : 0;
   g.mscale = turned ? rotation->mscale : 1.f;

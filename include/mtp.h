@@ -521,7 +521,8 @@ typedef struct mtp_paged_cache {
 /* A step's rows for a paged cache: k, v (and q) [R, L, heads, head_dim] bf16 with
  * strides in elements (0: those of dense tensors; multiples of 8, the last dimension
  * dense; k and v share theirs).  q and q_out are null, or the queries and where they go
- * turned, [R, L, n_heads, head_dim] dense (q_out may be a dense q).
+ * turned, [R, L, n_heads, head_dim] dense (q_out may be a dense q; it must not lie within
+ * what q, k and v span otherwise).
  *   ctx_len [R]: rows of request r once the step's are in; n_new [R] (nullable: L): how
  *   many those are, clamped to [0, L]: row i < n_new[r] goes to ctx_len[r] - n_new[r] + i.
  *   pos [R, L] (nullable: that index): positions for the rotation. */
