@@ -510,17 +510,19 @@ void append_launch(const AppendArgs& g, bool vec, bool inter, unsigned ctas, cud
 // 16 elements of keys and of values per thread, neighbouring threads along a row and
 // then over heads, as the dense rows lie.  Bound: HBM, 5.9 TB/s for large caches; 15000 rows of 8 heads
 // 12 to 17 us, length, page and row one after another.
-// kDense: rows behind a request's stay as they are, but for `more` of zeros (kv_dense_launch).
+// kDense: rows behind a request's stay as they are, but for `more` of zeros (kv_dense_launch); a request without new tokens has none.
 template <int HD, bool kF8, bool kDense>
 __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const mtp_paged_cache c, int T, const int32_t* __restrict__ ctx_len,
                                                              __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out, int L,
-                                                             const int32_t* __restrict__ n_new, int32_t* __restrict__ ctx_out) {
+                                                             const int32_t* __restrict__ n_new, int causal, int32_t* __restrict__ ctx_out) {
   constexpr int kUnits = HD / 16;
   const int r = blockIdx.y;
   int ctx = ctx_len[r], more = 0;
   if constexpr (kDense) {
     ctx = min(max(ctx, 0), c.table_len * c.page);
-    more = n_new ? L - min(max(n_new[r], 0), L) : 0;
+    const int fresh = n_new ? min(max(n_new[r], 0), L) : L;
+    if (fresh == 0) ctx = 0;
+    else if (causal) more = L - fresh;
     if (blockIdx.x == 0 && threadIdx.x == 0) ctx_out[r] = ctx + more;
   }
   const long long all = static_cast<long long>(kDense ? ctx + more : T) * c.n_kv_heads * kUnits, apart = static_cast<long long>(gridDim.x) * kThreads;
@@ -569,12 +571,12 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const mtp_paged_cac
 
 template <int HD, bool kDense>
 void gather_launch(const mtp_paged_cache& c, const dim3& grid, int T, const int32_t* ctx_len, void* k_out, void* v_out, int L,
-                   const int32_t* n_new, int32_t* ctx_out, cudaStream_t st) {
+                   const int32_t* n_new, int causal, int32_t* ctx_out, cudaStream_t st) {
   __nv_bfloat16 *k = static_cast<__nv_bfloat16*>(k_out), *v = static_cast<__nv_bfloat16*>(v_out);
   if (c.dtype == MTP_E4M3)
-    kv_gather_kernel<HD, true, kDense><<<grid, kThreads, 0, st>>>(c, T, ctx_len, k, v, L, n_new, ctx_out);
+    kv_gather_kernel<HD, true, kDense><<<grid, kThreads, 0, st>>>(c, T, ctx_len, k, v, L, n_new, causal, ctx_out);
   else
-    kv_gather_kernel<HD, false, kDense><<<grid, kThreads, 0, st>>>(c, T, ctx_len, k, v, L, n_new, ctx_out);
+    kv_gather_kernel<HD, false, kDense><<<grid, kThreads, 0, st>>>(c, T, ctx_len, k, v, L, n_new, causal, ctx_out);
 }
 
 mtp_status rotation_check(const mtp_rotation* rot, int head_dim) {
@@ -605,16 +607,16 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 }  // namespace
 
 mtp_status kv_dense_launch(const mtp_paged_cache& c, int R, int L, long long T, const int32_t* ctx_len, const int32_t* n_new,
-                           void* k_out, void* v_out, int32_t* ctx_out, cudaStream_t st) {
+                           bool causal, void* k_out, void* v_out, int32_t* ctx_out, cudaStream_t st) {
   const long long blocks = (T * c.n_kv_heads * (c.head_dim / 16) + kThreads - 1) / kThreads;
   if (T > 0x7FFFFFFFll || R > 65535) return MTP_ERR_UNSUPPORTED;
   // the lengths are the device's: some 16 CTAs per SM go over what there is
   const long long most = std::max(1ll, 16ll * sm_count_current() / R);
   const dim3 grid(static_cast<unsigned>(std::min(blocks, most)), static_cast<unsigned>(R));
   if (c.head_dim == 128)
-    gather_launch<128, true>(c, grid, static_cast<int>(T), ctx_len, k_out, v_out, L, n_new, ctx_out, st);
+    gather_launch<128, true>(c, grid, static_cast<int>(T), ctx_len, k_out, v_out, L, n_new, causal, ctx_out, st);
   else
-    gather_launch<64, true>(c, grid, static_cast<int>(T), ctx_len, k_out, v_out, L, n_new, ctx_out, st);
+    gather_launch<64, true>(c, grid, static_cast<int>(T), ctx_len, k_out, v_out, L, n_new, causal, ctx_out, st);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;
@@ -812,9 +814,9 @@ extern "C" mtp_status mtp_kv_gather(const mtp_paged_cache* cache, int R, int T, 
   if (blocks > 0x7FFFFFFFll) return MTP_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(R));
   if (cache->head_dim == 128)
-    gather_launch<128, false>(*cache, grid, T, ctx_len, k_out, v_out, 0, nullptr, nullptr, st);
+    gather_launch<128, false>(*cache, grid, T, ctx_len, k_out, v_out, 0, nullptr, 0, nullptr, st);
   else
-    gather_launch<64, false>(*cache, grid, T, ctx_len, k_out, v_out, 0, nullptr, nullptr, st);
+    gather_launch<64, false>(*cache, grid, T, ctx_len, k_out, v_out, 0, nullptr, 0, nullptr, st);
   note_launch();
   MTP_LAUNCH_CHECK();
   return MTP_OK;

@@ -28,10 +28,11 @@ struct PagedAttn {
   long long rec_stride = 0;
 };
 
-// The rows that a request holds as dense bf16 rows [R, T, Hkv, hd], those behind them left as they are but for
-// L - n_new[r] rows of zeros; ctx_out[r] = ctx_len[r] + L - n_new[r] (n_new null: ctx_len[r]).
+// The rows that a request holds as dense bf16 rows [R, T, Hkv, hd], those behind them left as they are but for, if causal,
+// L - n_new[r] rows of zeros; ctx_out[r] = ctx_len[r] and those (n_new null: L).  Nothing of a request with n_new[r] = 0:
+// ctx_out[r] = 0, its pages are not looked up.
 mtp_status kv_dense_launch(const mtp_paged_cache& c, int R, int L, long long T, const int32_t* ctx_len, const int32_t* n_new,
-                           void* k_out, void* v_out, int32_t* ctx_out, cudaStream_t stream);
+                           bool causal, void* k_out, void* v_out, int32_t* ctx_out, cudaStream_t st);
 
 bool paged_attn_sizes_ok(int R, int L, int H, const mtp_paged_cache& c);
 size_t paged_attn_workspace_bytes(int R, int L, int H, const mtp_paged_cache& c);

@@ -1538,7 +1538,7 @@ __global__ void __launch_bounds__(256) paged_hide_kernel(int L, int H, int hd, l
 mtp_status dense_launch(const PagedAttn& p, const Dense& d, uint8_t* ws, size_t ws_bytes, cudaStream_t st) {
   int32_t* ctx = reinterpret_cast<int32_t*>(ws + d.ctx);
   // not causal: every token sees all of the request's rows, and only those
-  mtp_status s = kv_dense_launch(p.c, p.R, p.L, d.T, p.ctx_len, p.causal ? p.n_new : nullptr, ws + d.k, ws + d.v, ctx, st);
+  mtp_status s = kv_dense_launch(p.c, p.R, p.L, d.T, p.ctx_len, p.n_new, p.causal, ws + d.k, ws + d.v, ctx, st);
   if (s != MTP_OK) return s;
   PrefixAttn a;
   a.R = p.R, a.L = p.L, a.H = p.H, a.Hkv = p.c.n_kv_heads, a.hd = p.c.head_dim, a.T = static_cast<int>(d.T);

@@ -585,7 +585,8 @@ size_t mtp_paged_attention_workspace_bytes(const mtp_paged_dims* dims, const mtp
  *   Rows that a token does not see may hold anything, NaN among it.  A value that is not
  *   finite, in a row that a token sees, makes its outputs of that dimension not finite.
  *   Pages outside [0, n_pages) set MTP_DEVERR_PAGE_RANGE and are not read; the outputs of
- *   requests that name them are of no use.
+ *   requests that name them are of no use.  Pages behind ctx_len[r], and those of a request with
+ *   n_new[r] = 0, are not looked up.
  *   q bf16, 16-byte aligned; out [R, L, n_heads, head_dim] bf16, apart from q; lse [R, L, n_heads]
  *   float, nullable: natural logarithm of the softmax's denominator, maximum included.
  *   ws: mtp_paged_attention_workspace_bytes bytes (null if 0), 16-byte aligned; calls that may
