@@ -782,11 +782,11 @@ extern "C" mtp_status mtp_kv_append(const mtp_paged_cache* cache, const mtp_kv_r
   g.rot = turned ? rotation->rot : 0;
   g.mscale = turned ? rotation->mscale : 1.f;
   g.inv_freq = turned ? rotation->inv_freq : nullptr;
-  g.kv_blocks = (w.L + 14) / 16 + 1;
+  g.kv_blocks = static_cast<int>((w.L + 14ll) / 16 + 1);
   g.kv_groups = (Hkv + kWarps - 1) / kWarps;
   g.kv_ctas = static_cast<long long>(w.R) * g.kv_blocks * g.kv_groups;
   g.q_groups = w.q ? (w.n_heads + kWarps - 1) / kWarps : 0;
-  g.q_chunks = (w.L + 15) / 16;
+  g.q_chunks = static_cast<int>((w.L + 15ll) / 16);
   const long long ctas = g.kv_ctas + static_cast<long long>(w.R) * g.q_chunks * g.q_groups;
   if (ctas > 0x7FFFFFFFll) return MTP_ERR_UNSUPPORTED;
   const bool inter = turned && rotation->interleaved, vec = g.rot % 16 == 0;

@@ -1,0 +1,35 @@
+"""mtp_kv_append at the ends of their sizes (no GPU: nothing is launched)."""
+import ctypes
+
+import pytest
+
+from deepseek_sequential_mtp_gb300 import build, lib as binding
+
+P = 1 << 20  # an address that nothing reads
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def cache(**kw):
+    c = binding.PagedCache(P, P, P, P, P, 8, 64, 4, 2, 128, binding.MTP_E4M3)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def rows(R, L, **kw):
+    w = binding.KvRows(R, L, 0, P, P)
+    w.ctx_len = P
+    for k, v in kw.items():
+        setattr(w, k, v)
+    return ctypes.byref(w)
+
+
+@pytest.mark.parametrize("L", [2147483647, 2147483634, 2147483633])
+def test_more_blocks_than_a_launch_has(lib, L):
+    """17 requests of that many rows: more CTAs than a grid holds, counted without passing 31 bits on the way."""
+    assert lib.mtp_kv_append(cache(), rows(17, L), None, None) == 7
