@@ -742,7 +742,7 @@ extern "C" mtp_status mtp_rope(long long N, int H, int head_dim, int dtype, cons
 
 extern "C" mtp_status mtp_kv_append(const mtp_paged_cache* cache, const mtp_kv_rows* rows, const mtp_rotation* rotation,
                                     cudaStream_t st) {
-  if (const mtp_status s = paged_cache_check(cache, true); s != MTP_OK) return s;
+  if (const mtp_status s = paged_cache_check(cache, false); s != MTP_OK) return s;
   if (!rows) return MTP_ERR_INVALID_ARG;
   AppendArgs g{};
   g.c = *cache;
@@ -752,7 +752,8 @@ extern "C" mtp_status mtp_kv_append(const mtp_paged_cache* cache, const mtp_kv_r
   if (w.R < 0 || w.L < 0 || w.n_heads < 0) return MTP_ERR_INVALID_ARG;
   if (const mtp_status s = rotation_check(rotation, hd); s != MTP_OK) return s;
   if ((w.q == nullptr) != (w.q_out == nullptr) || (w.q && w.n_heads < 1)) return MTP_ERR_INVALID_ARG;
-  if (w.R == 0 || w.L == 0) return MTP_OK;
+  if (w.R == 0 || w.L == 0) return MTP_OK;  // (a table without requests has no address)
+  if (const mtp_status s = paged_cache_check(cache, true); s != MTP_OK) return s;
   if (!w.k || !w.v || !w.ctx_len) return MTP_ERR_INVALID_ARG;
   if (!aligned16(w.k) || !aligned16(w.v) || !aligned16(w.q) || !aligned16(w.q_out)) return MTP_ERR_ALIGNMENT;
   if (!aligned4(w.ctx_len) || !aligned4(w.n_new) || !aligned4(w.pos)) return MTP_ERR_ALIGNMENT;
@@ -802,11 +803,12 @@ extern "C" mtp_status mtp_kv_append(const mtp_paged_cache* cache, const mtp_kv_r
 
 extern "C" mtp_status mtp_kv_gather(const mtp_paged_cache* cache, int R, int T, const int32_t* ctx_len, void* k_out, void* v_out,
                                     cudaStream_t st) {
-  if (const mtp_status s = paged_cache_check(cache, true); s != MTP_OK) return s;
+  if (const mtp_status s = paged_cache_check(cache, false); s != MTP_OK) return s;
   if (R < 0 || T < 0) return MTP_ERR_INVALID_ARG;
   if (R > 65535) return MTP_ERR_UNSUPPORTED;
   if (T > static_cast<long long>(cache->table_len) * cache->page) return MTP_ERR_SHAPE;
   if (R == 0 || T == 0) return MTP_OK;
+  if (const mtp_status s = paged_cache_check(cache, true); s != MTP_OK) return s;
   if (!ctx_len || !k_out || !v_out) return MTP_ERR_INVALID_ARG;
   if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(ctx_len)) return MTP_ERR_ALIGNMENT;
   const long long units = static_cast<long long>(T) * cache->n_kv_heads * (cache->head_dim / 16);

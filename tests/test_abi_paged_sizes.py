@@ -1,4 +1,4 @@
-"""mtp_kv_append at the ends of their sizes (no GPU: nothing is launched)."""
+"""mtp_kv_append, mtp_kv_gather at the ends of their sizes (no GPU: nothing is launched)."""
 import ctypes
 
 import pytest
@@ -33,3 +33,16 @@ def rows(R, L, **kw):
 def test_more_blocks_than_a_launch_has(lib, L):
     """17 requests of that many rows: more CTAs than a grid holds, counted without passing 31 bits on the way."""
     assert lib.mtp_kv_append(cache(), rows(17, L), None, None) == 7
+
+
+def test_a_batch_without_requests(lib):
+    """Its page table is an empty tensor, whose address is null."""
+    none = cache(page_table=None)
+    assert lib.mtp_kv_append(none, rows(0, 4), None, None) == 0
+    assert lib.mtp_kv_append(none, rows(0, 4, k=None, v=None, ctx_len=None), None, None) == 0
+    assert lib.mtp_kv_gather(none, 0, 16, None, None, None, None) == 0
+    for bad in (dict(page=24), dict(dtype=0), dict(head_dim=96)):  # what does not depend on the batch is still checked
+        assert lib.mtp_kv_append(cache(**bad), rows(0, 4), None, None) == 7
+        assert lib.mtp_kv_gather(cache(**bad), 0, 16, None, None, None, None) == 7
+    assert lib.mtp_kv_append(none, rows(2, 4), None, None) == 1
+    assert lib.mtp_kv_gather(none, 2, 16, P, P, P, None) == 1
