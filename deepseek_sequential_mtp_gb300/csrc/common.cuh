@@ -161,6 +161,10 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+// 2^e, exactly (0 below 2^-149); 2^127 above
+__device__ __forceinline__ float power_of_two(int e) {
+  return __int_as_float(e >= -126 ? (min(e, 127) + 127) << 23 : e >= -149 ? 1 << (e + 149) : 0);
+}
 // a / b for a >= 0, b > 0: of 32 bits where both fit (a 64-bit division is some hundred instructions)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (a | b) >> 32 ? a / b : static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));

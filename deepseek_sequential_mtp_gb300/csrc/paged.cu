@@ -244,9 +244,8 @@ __device__ __forceinline__ void unpack_e4m3(uint32_t w, float (&x)[4]) {
     x[2 * i + 1] = f.y;
   }
 }
-__device__ __forceinline__ float power_of_two(int e) {  // 2^e, 0 below the normal range
-  return e < -126 ? 0.f : __int_as_float((min(e, 127) + 127) << 23);
-}
+// exponent of a scale byte, 1..254 or taken as the nearest of those
+__device__ __forceinline__ int scale_exponent(uint8_t b) { return min(max(static_cast<int>(b), 1), 254) - 127; }
 
 // 16 bf16 elements of unit u of a row, as 8 words: the runs' (kVec), or pairs
 template <bool kVec, bool kInter>
@@ -340,7 +339,7 @@ __device__ __forceinline__ void append_rows(const uint32_t (&raw)[HD / 32][8], i
       }
     }
   } else {
-    const int was = begun ? 0 : static_cast<int>(*scale) - 127;
+    const int old = begun ? 0 : scale_exponent(*scale);
     float a[kIt][8], b[kIt][8], top = 0.f;
 #pragma unroll
     for (int i = 0; i < kIt; ++i) {
@@ -360,7 +359,6 @@ __device__ __forceinline__ void append_rows(const uint32_t (&raw)[HD / 32][8], i
     const uint32_t bits = __float_as_uint(top);
     int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -90);
     if (!begun) {
-      const int old = min(max(was, -126), 126);
       if (e > old) {  // rows that are there to the new scale
         const float f = power_of_two(old - e);
         const int first = slot & ~15;
@@ -542,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) kv_gather_kernel(const mtp_paged_cac
           const long long s = head * (c.page >> 4) + (slot >> 4);
           const uint4 kc = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + at);
           const uint4 vc = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + at);
-          const float ks = power_of_two(c.k_scale[s] - 127), vs = power_of_two(c.v_scale[s] - 127);
+          const float ks = power_of_two(scale_exponent(c.k_scale[s])), vs = power_of_two(scale_exponent(c.v_scale[s]));
           const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
           uint32_t* ko = reinterpret_cast<uint32_t*>(k);
           uint32_t* vo = reinterpret_cast<uint32_t*>(v);

@@ -42,9 +42,6 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // x 2^(2 e), f = 2^e: references of blocks whose scales are far apart differ by more than a float's exponent holds
 __device__ __forceinline__ float scale_twice(float x, float f) { return x * f * f; }
-__device__ __forceinline__ float power_of_two(int e) {  // 2^e within the normal range
-  return __int_as_float((min(max(e, -126), 127) + 127) << 23);
-}
 // tiled four-dimensional tensor copy global -> shared; x is the inner coordinate
 __device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
   asm volatile(

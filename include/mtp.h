@@ -506,7 +506,7 @@ mtp_status mtp_rope(long long N, int H, int head_dim, int dtype, const mtp_rotat
  *   dtype MTP_BF16: bf16 rows; k_scale and v_scale are not read.
  *   dtype MTP_E4M3: codes as in mtp_fp8_matrix, and for every 16 rows of a page and
  *   head one power of two: k_scale, v_scale [n_pages, n_kv_heads, page / 16] bytes b,
- *   1..254, for 2^(b - 127); a value is code * 2^(b - 127), exactly.  mtp_paged_attention
+ *   1..254 (others are taken as the nearest), for 2^(b - 127); a value is code * 2^(b - 127), exactly.  mtp_paged_attention
  *   takes v_scale within 27..227, as mtp_kv_append makes it of values up to 2^108.
  * page_table [R, table_len] int32.  Tensors are 16-byte aligned, the scales and the
  * table 4-byte aligned.  A page may stand in several requests' tables (a shared prompt).
