@@ -71,6 +71,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "attn_steps.cuh"
 #include "gemm_tc.cuh"
 #include "mbarrier.cuh"
 #include "prefix_attn.cuh"
@@ -83,8 +84,6 @@ namespace {
 
 constexpr int kRows = 128;   // rows per tile (MMA M, TMEM lanes)
 constexpr int kKeys = 128;   // keys per block
-constexpr float kStaleMaxLog2 = 8.0f;  // a running maximum is replaced only when exceeded by 2^8
-constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 // costs for the deal: a block with one row tile, with two, and what a segment
 // of a request's own cache costs besides
 constexpr int kCostOne = 6, kCostTwo = 11, kCostItem = 5;
@@ -92,19 +91,7 @@ constexpr int kCostOne = 6, kCostTwo = 11, kCostItem = 5;
 // prefix on row tiles; log2 of its blocks' keys, keys of a box
 constexpr int kSmallPrefix = 16, kSmallOwn = 32, kSmallOwnBeside = 8, kSmallShift = 6, kSmallBox = 32, kSmallCost = 2, kSmallCostItem = 1;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
-// tiled four-dimensional tensor copy global -> shared; x is the inner coordinate
-__device__ __forceinline__ void tma_tile_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-      : "memory");
-}
 
 __host__ __device__ constexpr int blocks_of(int keys, int shift) { return (keys + (1 << shift) - 1) >> shift; }
 
@@ -700,23 +687,6 @@ prefix_attn_kernel(const __grid_constant__ Maps maps, const Shape sh, float scal
 // ---------------------------------------------------------------------------
 // Own caches with few rows per key head
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // the 16-byte piece with element (row, col) of rows of 64 elements that TMA wrote with the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz(uint32_t box, int row, int col) {
   return box + row * 128 + ((((col >> 3) ^ row) & 7) << 4);
