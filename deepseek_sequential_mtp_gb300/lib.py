@@ -1034,6 +1034,8 @@ def rope(x: torch.Tensor, pos: torch.Tensor, inv_freq: torch.Tensor, mscale: flo
 def _paged(k_pages, v_pages, page_table, k_scale, v_scale, device) -> PagedCache:
     """ctypes view of a paged cache: pages [n, Hkv, page, hd] bf16, or uint8 e4m3 codes with
     exponents [n, Hkv, page / 16] uint8."""
+    if k_pages is None or v_pages is None or page_table is None:
+        raise MtpError(f"{'k_pages' if k_pages is None else 'v_pages' if v_pages is None else 'page_table'} is missing")
     if k_pages.dim() != 4 or k_pages.dtype not in (torch.bfloat16, torch.uint8):
         raise MtpError("k_pages must be bfloat16 or uint8 [pages, kv_heads, page, hd]")
     shape = k_pages.shape

@@ -48,3 +48,17 @@ def test_the_tensors_live_as_long_as_the_step(eight, gamma):
     del step
     gc.collect()
     assert all(t() is None for t in seen.values())
+
+
+@pytest.mark.parametrize("name", ["k_pages", "v_pages", "page_table"])
+@pytest.mark.parametrize("how", ["missing", "none"])
+def test_a_cache_without_its_tensors_is_refused(name, how):
+    cfg = replace(synth.DRAFT_SMALL, ctx=320)
+    w = synth.make_draft_inputs(cfg, 1)["weights"]
+    c = cache(cfg, 32, False)
+    if how == "none":
+        c[name] = None
+    else:
+        del c[name]
+    with pytest.raises(lib.MtpError, match=name):
+        lib.DraftStep(cfg, w, device="cpu", paged=c)
