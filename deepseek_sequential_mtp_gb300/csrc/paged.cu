@@ -395,7 +395,7 @@ __device__ __forceinline__ void append_rows(const uint32_t (&raw)[HD / 32][8], i
   }
 }
 
-// Bound: HBM for many rows (32 requests x 8192 rows of 56 heads of 128: bf16 2.48 ms, 6.05 TB/s; e4m3 2.31 ms, 4.9 TB/s, with
+// Bound: HBM for many rows (32 requests x 8192 rows of 56 heads of 128: bf16 2.49 ms, 6.0 TB/s; e4m3 2.25 ms, 5.0 TB/s, with
 // its quantising), for few of them the chain from lengths over the table to the rows, 7 us of a
 // step's token of 32 requests, 9 us of 8 bits, whose block is read, scaled anew and written.
 // A CTA takes a block of 16 rows of a request and 8 heads, a warp per head (keys and

@@ -12,7 +12,7 @@
 //
 // Short tables and few items: a CTA per item, one launch (paged_item_kernel: loads that wait for one another).  Else three kernels, by
 // what bounds each: 8 bits on tcgen05 (paged_cols_kernel: HBM, 32 requests of 56 heads and 6500 keys
-// on average 437 us, 6.25 TB/s of codes; with 20 rows per key head the softmax of a block, 118 us where the bytes take
+// on average 441 us, 6.3 TB/s of codes; with 20 rows per key head the softmax of a block, 120 us where the bytes take
 // 60), bf16 on mma.sync from a ring of 16 keys per warp (paged_rows_kernel: launch and first loads for
 // small caches, HBM for large ones), many rows as gathered bf16 rows through the attention over own caches
 // (below), whose products are the bound.
@@ -1462,9 +1462,18 @@ mtp_status launch(const PagedAttn& p, const Shape& s, const Layout& l, uint8_t* 
 namespace {
 
 // Many rows: the requests' rows are gathered as dense bf16 rows, exactly, and go through the attention over own caches
-// (prefix_attn.cu), whose 128 rows share a block of keys: 1024 tokens of two requests, 4 heads per key head and 8000 tokens
-// and 8 bits 324 us instead of 877, 256 tokens (1024 rows) 107 instead of 250, 64 91 (172), 32 75 (128), 16 (64 rows) 118 (131);
-// bf16 318 us instead of 1638, then 106 (398), 92 (220), 77 (117), 123 (128).  Only where the copy is at most 4 GB.
+// (prefix_attn.cu), whose 128 rows share a block of keys.  Gathered, and in brackets tile by tile by the kernels above, us of a call out
+// of a cold cache, hd 128, 8 key heads:
+//   two requests of 8000 rows, 4 heads per key head    8 bits       bf16
+//     1024 tokens (4096 rows per key head)             381 (882)    387 (2204)
+//     256, 64                                          127 (236), 62 (82)    131 (538), 68 (142)
+//     32, 16 (128, 64 rows)                            56 (58), 52 (38)      59 (80), 55 (52)
+//   4096 rows each, 8 heads per key head
+//     8 tokens (64 rows) of 8, 32, 64 requests         82 (55), 258 (154), 487 (284)    91 (88), 303 (315), 578 (619)
+//     12 tokens                                        84 (68), 264 (200), 502 (371)    94 (140), 309 (522), 588 (1026)
+//     16 tokens                                        86 (91), 274 (279), 514 (532)    95 (144), 315 (531), 601 (1049)
+// So bf16 gains from 64 rows on, 8 bits from 128; between the two 8 bits pay up to 1.7 times here, for weights of 2^-15 instead of
+// 2^-11.  Only where the copy is at most 4 GB.
 constexpr int kDenseRows = 64;
 constexpr unsigned long long kDenseMost = 1ull << 32;
 

@@ -595,10 +595,11 @@ size_t mtp_paged_attention_workspace_bytes(const mtp_paged_dims* dims, const mtp
  * products as they are; q is two codes and a power of two per row (exact above 2^-9 of
  * the row's largest element, off by 2^-17 of it below); a softmax weight is rounded to
  * fp16 (2^-11) and is three codes, off by 2^-26 of the largest p 2^E among
- * the keys that a part of the kernel takes one after another, at the most: weights below half of that leave the outputs (not
+ * the keys that a part of the kernel takes one after another, at the most: weights below that leave the outputs (not
  * the sums), n of them less than n 2^-26 of the largest.  MTP_BF16, and both where no workspace is needed or L * n_heads / n_kv_heads is 64 or more (and a copy
  * of the rows as bf16 in the workspace at most 4 GB): q, keys and values as they are, a softmax
- * weight as two bf16 parts (2^-15). */
+ * weight as two bf16 parts (2^-15).  Which kernel a call takes follows from the sizes alone, table_len
+ * among them, not from the lengths: a call repeated gives the same bits, one with a wider table may differ within these bounds. */
 mtp_status mtp_paged_attention(const mtp_paged_dims* dims, const mtp_paged_cache* cache, const void* q,
                                const int32_t* ctx_len, const int32_t* n_new, void* out, float* lse, void* ws,
                                size_t ws_bytes, cudaStream_t stream);
